@@ -40,8 +40,8 @@ def listed():
         dict(name="product-short", op="product", m=333, n=2560, k=10240, tile=True, out="bf16", fmt="e4m3"),
         # a training batch through the widest projection
         dict(name="product-forward", op="product", m=8192, n=16384, k=4096, tile=True, out="bf16", fmt="e4m3"),
-        # a weight's gradient in 32 bits over an odd number of tokens: both operands scaled by rows
-        dict(name="product-weight-grad", op="product", m=10240, n=2560, k=4093, tile=False, out="fp32", fmt="e5m2"),
+        # a weight's gradient over an odd number of tokens: both operands scaled by rows
+        dict(name="product-weight-grad", op="product", m=10240, n=2560, k=4093, tile=False, out="bf16", fmt="e5m2"),
         # one token through the gated block: both weights are read once
         dict(name="gated-one-token", op="gated", rows=1, d=4096, f=16384, act="silu", x="bf16", save=False),
         # an odd batch in fp16, with what the backward pass needs
@@ -70,8 +70,7 @@ def draw(rng):
             tile = rng.random() < 0.6
             c = dict(op=op, m=_spread(rng, 1, 16384), n=_spread(rng, 64, 16384),
                      k=_spread(rng, 128, 16384, 16) if tile else _spread(rng, 128, 16384), tile=tile,
-                     out=rng.choice(["bf16", "fp16"]) if tile else rng.choice(["bf16", "fp32"]),
-                     fmt=rng.choice(["e4m3", "e5m2"]))
+                     out=rng.choice(["bf16", "bf16", "fp16"]), fmt=rng.choice(["e4m3", "e5m2"]))
             size = c["m"] * c["n"] * c["k"]
         else:
             c = dict(op=op, rows=_spread(rng, 1 if op == "gated" else 64, 16384), d=_spread(rng, 256, 4096, 8),
