@@ -5,6 +5,11 @@ AMD Instinct MI355X (gfx950).
 The step runs in libopt8.so (hand-written HIP kernels behind a C ABI, declared
 in include/opt8.h); `opt8` is its ctypes binding (argument marshalling only).
 torch supplies device memory and streams only.
+
+`precision_optimizer_step_amd.opt8_products` (include/opt8_products.h) has the
+operators between the weights and their gradients: 8-bit block-scaled quantiser
+and matrix product, gated feed-forward block and its backward pass.  It is
+imported on its own (it needs torch at import, this package does not).
 """
 from .opt8 import (  # noqa: F401
     OPT8_BLOCK, OPT8_FP32_STATE_THRESHOLD, OPT8_STATE_8BIT, OPT8_STATE_BF16_SR, OPT8_STATE_FP32,

@@ -10,7 +10,9 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB = os.path.join(HERE, "libopt8.so")
 SOURCES = [os.path.join(HERE, "csrc", "opt8_host.cpp"), os.path.join(HERE, "csrc", "opt8_tables.cpp"),
-           os.path.join(HERE, "csrc", "opt8_kernels.hip"), os.path.join(HERE, "csrc", "opt8_map.hip")]
+           os.path.join(HERE, "csrc", "opt8_kernels.hip"), os.path.join(HERE, "csrc", "opt8_map.hip"),
+           os.path.join(HERE, "csrc", "products_host.cpp"), os.path.join(HERE, "csrc", "fp8_quantize.hip"),
+           os.path.join(HERE, "csrc", "fp8_product.hip"), os.path.join(HERE, "csrc", "gated_ffn.hip")]
 # bandwidth probe used by bench.py for the attainable-bandwidth context figure
 PROBE_LIB = os.path.join(HERE, "libopt8_probe.so")
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "bw_probe.hip")]

@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/opt8.h"
+#include "opt8_error.h"
 #include "opt8_host_limits.h"
 #include "opt8_internal.h"
 #include "opt8_map.h"
@@ -617,6 +618,9 @@ extern "C" int32_t opt8_default_mode(int64_t numel) {
 }
 
 extern "C" const char* opt8_last_error(void) { return t_error; }
+
+void opt8::clear_last_error() { t_error[0] = '\0'; }
+int opt8::set_last_error(int code, const char* message) { return fail(code, "%s", message); }
 
 namespace opt8 {
 namespace {
