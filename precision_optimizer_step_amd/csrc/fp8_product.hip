@@ -30,11 +30,15 @@ struct Product {
   bool vec;      // C takes 16-byte stores
 };
 
+// (The body is for the device pass alone: the host pass of this compiler
+// otherwise leaves out the launch stubs of some instances.)
+//
 // One BM x BN tile of C, WM x WN waves.  The scales of a step's block of k lie
 // in LDS beside its operand tiles, one for each row of either (TILE scales are
 // spread over their rows by the loads' addresses).
 template <int FA, class C, bool TILE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product p) {
+#if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = WM * WN;
   constexpr int MT = BM / WM / 16;
   static_assert(BN / WN == 64, "a wave takes 64 columns");
@@ -66,8 +70,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
 
   auto issue = [&](int step) {
     char* to = lds[step & 1];
-    la.issue(to, step, kbytes);
-    lb.issue(to + BM * kStepBytes, step, kbytes);
+    la.at_step(step, p.k - step * kStepBytes);
+    lb.at_step(step, p.k - step * kStepBytes);
+#pragma unroll
+    for (int j = 0; j < BM / 8 / NW; ++j) la.issue(lds_address(to), j);
+#pragma unroll
+    for (int j = 0; j < BN / 8 / NW; ++j) lb.issue(lds_address(to + BM * kStepBytes), j);
     if (scales)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(sbase + step * sstep * 4, sstep * 4),
                                                (lds_void*)(to + kTile + wave * 256), 4, soff, 0, 0, 0);
@@ -145,6 +153,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
       store8<C>(p.c + m * p.ldc + n, v, p.n - n, p.vec);
     }
   }
+#endif
 }
 
 // Few rows (one token to a short prompt): the time is that of reading B, so

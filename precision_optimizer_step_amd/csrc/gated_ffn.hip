@@ -1,4 +1,7 @@
 // Gated feed-forward block: h = act(x Wg^T) * (x Wu^T), and its backward pass.
+//
+// The bodies of the tiled kernels are for the device pass alone: the host pass of
+// this compiler otherwise leaves out the launch stubs of some of their instances.
 #include <algorithm>
 #include <type_traits>
 
@@ -20,12 +23,13 @@ constexpr float kTanhA = 0.7978845608028654f;    // sqrt(2/pi)
 constexpr float kTanhB = 0.044715f;
 
 // Value and slope of the activation.  tanh form: (1 + tanh y)/2 = sigmoid(2y).
-__device__ __forceinline__ void activate(float g, int act, float& value, float& slope) {
-  if (act == OPT8_ACT_SILU) {
+template <int ACT>
+__device__ __forceinline__ void activate(float g, float& value, float& slope) {
+  if constexpr (ACT == OPT8_ACT_SILU) {
     const float p = sigmoid(g);
     value = g * p;
     slope = p * __builtin_fmaf(g, 1.0f - p, 1.0f);
-  } else if (act == OPT8_ACT_GELU) {
+  } else if constexpr (ACT == OPT8_ACT_GELU) {
     const float below = 0.5f * erfcf(-0.70710678118654752f * g);
     value = g * below;
     slope = __builtin_fmaf(g * 0.39894228040143268f, exp_fast(-0.5f * g * g), below);
@@ -36,62 +40,19 @@ __device__ __forceinline__ void activate(float g, int act, float& value, float& 
     slope = __builtin_fmaf(2.0f * g * p * (1.0f - p), kTanhA * __builtin_fmaf(3.0f * kTanhB * g, g, 1.0f), p);
   }
 }
-__device__ __forceinline__ float activate(float g, int act) {
+template <int ACT>
+__device__ __forceinline__ float activate(float g) {
   float value, slope;
-  activate(g, act, value, slope);
+  activate<ACT>(g, value, slope);
   return value;
 }
-
-// ------------------------------------------------------------- tiled products
-// The steps of one tile: both operands' loads are queued by issue(step), A lies
-// first in a copy.  acc[q][j]: matrix tile q of the wave's two 32-column groups
-// (n side), matrix tile j of its rows.
-template <class T, Layout LA, Layout LB, int BM, int BN, int WM, class Issue, class Last>
-__device__ __forceinline__ void multiply(char (*lds)[(BM + BN) * kStepBytes], int first, int steps,
-                                         int mrow, int ncol0, int ncol1, Issue&& issue, Last&& last,
-                                         f32x4 (&acc)[4][BM / WM / 16]) {
-  constexpr int MT = BM / WM / 16;
-  Reader<LA, BM, MT / 2> ra;
-  Reader<LB, BN, 1> rb0, rb1;
-  ra.init(mrow);
-  rb0.init(ncol0);
-  rb1.init(ncol1);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  if (steps > 0) issue(first, lds[0]);
-  for (int s = 0; s < steps; ++s) {
-    wait_and_meet();
-    if (s + 1 < steps) issue(first + s + 1, lds[(s + 1) & 1]);
-    char* t = lds[s & 1];
-    if (s + 1 == steps) last(t);
-    const char* tb = t + BM * kStepBytes;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      i32x4 b[4] = {rb0.read(tb, 0, h), rb0.read(tb, 1, h), rb1.read(tb, 0, h), rb1.read(tb, 1, h)};
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const i32x4 a = ra.read(t, j, h);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q][j] = mfma16<T>(b[q], a, acc[q][j]);
-      }
-    }
-  }
-}
-
-// m (within the workgroup's tile) of matrix tile j, for this lane.
-__device__ __forceinline__ int row_of(int mrow, int j) {
-  const int lane = threadIdx.x & 63;
-  return mrow + (j >> 1) * 32 + 4 * (j & 1) + 8 * ((lane & 15) >> 2) + (lane & 3);
-}
-template <int MT>
-__device__ __forceinline__ void take8(const f32x4 (&acc)[4][MT], int group, int j, float* v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = acc[2 * group][j][i];
-    v[4 + i] = acc[2 * group + 1][j][i];
-  }
+// Calls f with the activation as a constant: the choice is made once, so that
+// the chains of neighbouring values overlap.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if (act == OPT8_ACT_SILU) f(std::integral_constant<int, OPT8_ACT_SILU>{});
+  else if (act == OPT8_ACT_GELU) f(std::integral_constant<int, OPT8_ACT_GELU>{});
+  else f(std::integral_constant<int, OPT8_ACT_GELU_TANH>{});
 }
 
 struct Forward {
@@ -108,56 +69,67 @@ struct Forward {
   bool vec;
 };
 
-// A BM x BN tile of B holds BN/2 rows of Wg and the same rows of Wu; a wave
-// takes 32 of each, so g and u of one h meet in one lane.
-template <class T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void gated_forward_kernel(const Forward p) {
-  constexpr int NW = WM * WN, MT = BM / WM / 16, HALF = BN / 2;
-  static_assert(BN / WN == 64 && NW % 2 == 0, "");
-  __shared__ __align__(16) char lds[2][(BM + BN) * kStepBytes];
+// A tile holds B/2 rows of Wg and the same rows of Wu beside B rows of x; a
+// wave takes as many columns of one as of the other, so g and u of one h meet
+// in one lane.
+template <class T, int B>
+__global__ __launch_bounds__(256, B == 256 ? 1 : 2) void gated_forward_kernel(const Forward p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int T16 = B / 32, HALF = B / 2;
+  __shared__ __align__(16) char lds[2][2 * B * kStepBytes];
   int tm, tn;
   tile_of_group(p.tiles_m, p.tiles_n, p.band, tm, tn);
   const int wave = wave_id(), lane = threadIdx.x & 63;
-  const int mrow = (wave / WN) * (BM / WM), wn = wave % WN;
-  const int m0 = tm * BM, f0 = tn * HALF;
+  const int mrow = (wave >> 1) * HALF, ncol = (wave & 1) * (HALF / 2);
+  const int m0 = tm * B, f0 = tn * HALF;
   const int64_t kbytes = 2 * int64_t{p.d}, kround = (kbytes + 15) & ~int64_t{15};
-  Loader<kRows, BM, NW> la;
-  Loader<kRows, HALF, NW / 2> lb;
-  la.init(p.x + m0 * p.ldx, p.ldx, (std::min(BM, p.rows - m0) - 1) * p.ldx + kround, 0, wave);
-  const bool second = wave >= NW / 2;
-  lb.init((second ? p.wu : p.wg) + f0 * p.ldw, p.ldw, (std::min(HALF, p.f - f0) - 1) * p.ldw + kround, 0,
-          second ? wave - NW / 2 : wave);
-  const int bto = (BM + (second ? HALF : 0)) * kStepBytes;
-  auto issue = [&](int step, char* to) {
-    la.issue(to, step, kbytes);
-    lb.issue(to + bto, step, kbytes);
+  Loader<kRows, B, 4> la;
+  Loader<kRows, HALF, 2> lb;
+  la.init(p.x + m0 * p.ldx, p.ldx, (std::min(B, p.rows - m0) - 1) * p.ldx + kround, 0, wave);
+  const bool second = wave >= 2;
+  lb.init((second ? p.wu : p.wg) + f0 * p.ldw, p.ldw, (std::min(HALF, p.f - f0) - 1) * p.ldw + kround, 0, wave & 1);
+  const int bto = (B + (second ? HALF : 0)) * kStepBytes;
+  auto at_step = [&](int step) {
+    const int left = static_cast<int>(kbytes) - step * kStepBytes;
+    la.at_step(step, left);
+    lb.at_step(step, left);
+  };
+  auto issue = [&](int j, uint32_t to, int i) {
+    if (i == 0) la.issue(to, j);
+    else lb.issue(to + bto, j);
   };
   const int steps = static_cast<int>((kbytes + kStepBytes - 1) / kStepBytes);
   auto last = [&](char* t) {
     if (kbytes & 15) {
-      clear_part_chunk<BM + BN, 64 * NW>(t, static_cast<int>(kbytes - (steps - 1) * kStepBytes));
+      clear_part_chunk<2 * B, 256>(t, static_cast<int>(kbytes - (steps - 1) * kStepBytes));
       __syncthreads();
     }
   };
-  f32x4 acc[4][MT];
-  multiply<T, kRows, kRows, BM, BN, WM>(lds, 0, steps, mrow, wn * 32, HALF + wn * 32, issue, last, acc);
+  f32x4 acc[T16][T16];
+  multiply<T, kRows, kRows, B, B, 2, 2>(lds, 0, steps, mrow, ncol, HALF + ncol, at_step, issue, last, acc);
 
-  const int n = f0 + wn * 32 + 8 * (lane >> 4);
+  with_act(p.act, [&](auto act) {
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int64_t m = m0 + row_of(mrow, j);
-    if (m >= p.rows) continue;
-    float g[8], u[8], h[8];
-    take8(acc, 0, j, g);
-    take8(acc, 1, j, u);
+    for (int j = 0; j < T16; ++j) {
+      const int64_t m = m0 + row_of(mrow, j);
+      if (m >= p.rows) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = activate(g[i], p.act) * u[i];
-    store8<T>(p.h + m * p.ldh + n, h, p.f - n, p.vec);
-    if (p.gate) {
-      store8<T>(p.gate + m * p.ldg + n, g, p.f - n, p.vec);
-      store8<T>(p.up + m * p.ldg + n, u, p.f - n, p.vec);
+      for (int q = 0; q < T16 / 4; ++q) {
+        const int n = f0 + ncol + 32 * q + 8 * (lane >> 4);
+        float g[8], u[8], h[8];
+        take8(acc, q, j, g);
+        take8(acc, q + T16 / 4, j, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = activate<decltype(act)::value>(g[i]) * u[i];
+        store8<T>(p.h + m * p.ldh + n, h, p.f - n, p.vec);
+        if (p.gate) {
+          store8<T>(p.gate + m * p.ldg + n, g, p.f - n, p.vec);
+          store8<T>(p.up + m * p.ldg + n, u, p.f - n, p.vec);
+        }
+      }
     }
-  }
+  });
+#endif
 }
 
 // Few rows: the time is that of reading both weights.  A workgroup owns 16
@@ -225,7 +197,9 @@ __global__ __launch_bounds__(256) void gated_forward_few_kernel(const Forward p)
     for (int i = 0; i < 4; ++i) {
       const int n = n0 + 4 * g + i;
       if (n >= p.f) continue;
-      p.h[m * p.ldh + n] = static_cast<uint16_t>(bits_of(T{}, activate(t[0][i], p.act) * t[1][i]));
+      float value = 0.0f;
+      with_act(p.act, [&](auto act) { value = activate<decltype(act)::value>(t[0][i]); });
+      p.h[m * p.ldh + n] = static_cast<uint16_t>(bits_of(T{}, value * t[1][i]));
       if (p.gate) {
         p.gate[m * p.ldg + n] = static_cast<uint16_t>(bits_of(T{}, t[0][i]));
         p.up[m * p.ldg + n] = static_cast<uint16_t>(bits_of(T{}, t[1][i]));
@@ -280,58 +254,58 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(const Backward p) {
           rc[i] = c[i];
         }
     }
+    with_act(p.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float dh = value_of<T>(static_cast<uint16_t>(ra[i]));
-      float value, slope;
-      activate(value_of<T>(static_cast<uint16_t>(rb[i])), p.act, value, slope);
-      dg[i] = dh * value_of<T>(static_cast<uint16_t>(rc[i])) * slope;
-      du[i] = dh * value;
-    }
+      for (int i = 0; i < 8; ++i) {
+        const float dh = value_of<T>(static_cast<uint16_t>(ra[i]));
+        float value, slope;
+        activate<decltype(act)::value>(value_of<T>(static_cast<uint16_t>(rb[i])), value, slope);
+        dg[i] = dh * value_of<T>(static_cast<uint16_t>(rc[i])) * slope;
+        du[i] = dh * value;
+      }
+    });
     uint16_t* o = reinterpret_cast<uint16_t*>(p.both) + m * 2 * p.width + n;
     store8<T>(o, dg, 8, true);
     store8<T>(o + p.width, du, 8, true);
   }
 }
 
-// (The bodies of the next two are for the device pass alone: the host pass of
-// this compiler leaves out the stubs of some of their instances otherwise.)
-//
 // dx = [dg du] [Wg; Wu]: k runs along the rows of the weights.
-template <class T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void gated_dx_kernel(const Backward p) {
+template <class T, int B>
+__global__ __launch_bounds__(256, B == 256 ? 1 : 2) void gated_dx_kernel(const Backward p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int NW = WM * WN, MT = BM / WM / 16;
-  static_assert(BN / WN == 64, "");
-  __shared__ __align__(16) char lds[2][(BM + BN) * kStepBytes];
+  constexpr int T16 = B / 32, HALF = B / 2;
+  __shared__ __align__(16) char lds[2][2 * B * kStepBytes];
   int tm, tn;
   tile_of_group(p.tiles_m, p.tiles_n, p.band, tm, tn);
   const int wave = wave_id(), lane = threadIdx.x & 63;
-  const int mrow = (wave / WN) * (BM / WM), wn = wave % WN;
-  const int64_t m0 = int64_t{tm} * BM;
-  const int n0 = tn * BN;
-  const int64_t lda = 4 * p.width, kbytes = lda;
-  Loader<kRows, BM, NW> la;
-  Loader<kCols, BN, NW> lg, lu;
-  la.init(p.both + m0 * lda, lda, std::min<int64_t>(BM, p.rows - m0) * lda, 0, wave);
-  const int64_t climit = (p.f - 1) * p.ldw + ((2 * int64_t{p.d} + 15) & ~int64_t{15}) - 2 * n0;
-  lg.init(p.wg + 2 * n0, p.ldw, climit, p.d - n0, wave);
-  lu.init(p.wu + 2 * n0, p.ldw, climit, p.d - n0, wave);
+  const int mrow = (wave >> 1) * HALF, ncol = (wave & 1) * HALF;
+  const int64_t m0 = int64_t{tm} * B;
+  const int n0 = tn * B;
+  const int64_t lda = 4 * p.width;
+  Loader<kRows, B, 4> la;
+  Loader<kCols, B, 4> lb;
+  la.init(p.both + m0 * lda, lda, std::min<int64_t>(B, p.rows - m0) * lda, 0, wave);
+  lb.init(p.wg + 2 * n0, p.ldw, (p.f - 1) * p.ldw + ((2 * int64_t{p.d} + 15) & ~int64_t{15}) - 2 * n0, p.d - n0, wave);
   const int half = static_cast<int>(p.width / 64);
-  auto issue = [&](int step, char* to) {
-    la.issue(to, step, kbytes);
-    if (step < half) lg.issue(to + BM * kStepBytes, step, 0);
-    else lu.issue(to + BM * kStepBytes, step - half, 0);
+  auto at_step = [&](int step) {
+    la.at_step(step, (2 * half - step) * kStepBytes);
+    lb.base = (step < half ? p.wg : p.wu) + 2 * n0;
+    lb.at_step(step < half ? step : step - half, 0);
   };
-  f32x4 acc[4][MT];
-  multiply<T, kRows, kCols, BM, BN, WM>(lds, 0, 2 * half, mrow, wn * 64, wn * 64 + 32, issue, [](char*) {}, acc);
+  auto issue = [&](int j, uint32_t to, int i) {
+    if (i == 0) la.issue(to, j);
+    else lb.issue(to + B * kStepBytes, j);
+  };
+  f32x4 acc[T16][T16];
+  multiply<T, kRows, kCols, B, B, 2, 2>(lds, 0, 2 * half, mrow, ncol, ncol + HALF / 2, at_step, issue, [](char*) {}, acc);
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
+  for (int j = 0; j < T16; ++j) {
     const int64_t m = m0 + row_of(mrow, j);
     if (m >= p.rows) continue;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int n = n0 + wn * 64 + 32 * q + 8 * (lane >> 4);
+    for (int q = 0; q < T16 / 2; ++q) {
+      const int n = n0 + ncol + 32 * q + 8 * (lane >> 4);
       float v[8];
       take8(acc, q, j, v);
       store8<T>(p.dx + m * p.lddx + n, v, p.d - n, p.vec);
@@ -341,40 +315,42 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gated_dx_kernel(const Backwar
 }
 
 // dWg = dg^T x and dWu = du^T x: k is the rows (tokens) of both operands.
-template <class T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void gated_dw_kernel(const Backward p) {
+template <class T, int B>
+__global__ __launch_bounds__(256, B == 256 ? 1 : 2) void gated_dw_kernel(const Backward p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int NW = WM * WN, MT = BM / WM / 16;
-  static_assert(BN / WN == 64, "");
-  __shared__ __align__(16) char lds[2][(BM + BN) * kStepBytes];
+  constexpr int T16 = B / 32, HALF = B / 2;
+  __shared__ __align__(16) char lds[2][2 * B * kStepBytes];
   int tm, tn;
   tile_of_group(p.tiles_m, p.tiles_n, p.band, tm, tn);
   const int wave = wave_id(), lane = threadIdx.x & 63;
-  const int mrow = (wave / WN) * (BM / WM), wn = wave % WN;
+  const int mrow = (wave >> 1) * HALF, ncol = (wave & 1) * HALF;
   const int one = p.tiles_m / 2;
   const bool second = tm >= one;
-  const int f0 = (second ? tm - one : tm) * BM, n0 = tn * BN;
+  const int f0 = (second ? tm - one : tm) * B, n0 = tn * B;
   const int64_t lda = 4 * p.width;
-  Loader<kCols, BM, NW> la;
-  Loader<kCols, BN, NW> lb;
+  Loader<kCols, B, 4> la, lb;
   const int64_t off = 2 * (f0 + (second ? p.width : 0));
-  la.init(p.both + off, lda, p.rows * lda - off, p.width - f0, wave);
+  la.init(p.both + off, lda, p.rows * lda - off, static_cast<int>(p.width) - f0, wave);
   lb.init(p.x + 2 * n0, p.ldx, (p.rows - 1) * p.ldx + ((2 * int64_t{p.d} + 15) & ~int64_t{15}) - 2 * n0, p.d - n0, wave);
-  auto issue = [&](int step, char* to) {
-    la.issue(to, step, 0);
-    lb.issue(to + BM * kStepBytes, step, 0);
+  auto at_step = [&](int step) {
+    la.at_step(step, 0);
+    lb.at_step(step, 0);
+  };
+  auto issue = [&](int j, uint32_t to, int i) {
+    if (i == 0) la.issue(to, j);
+    else lb.issue(to + B * kStepBytes, j);
   };
   const int steps = static_cast<int>((p.rows + 63) / 64);
-  f32x4 acc[4][MT];
-  multiply<T, kCols, kCols, BM, BN, WM>(lds, 0, steps, mrow, wn * 64, wn * 64 + 32, issue, [](char*) {}, acc);
+  f32x4 acc[T16][T16];
+  multiply<T, kCols, kCols, B, B, 2, 2>(lds, 0, steps, mrow, ncol, ncol + HALF / 2, at_step, issue, [](char*) {}, acc);
   uint16_t* out = second ? p.dwu : p.dwg;
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
+  for (int j = 0; j < T16; ++j) {
     const int64_t m = f0 + row_of(mrow, j);
     if (m >= p.f) continue;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int n = n0 + wn * 64 + 32 * q + 8 * (lane >> 4);
+    for (int q = 0; q < T16 / 2; ++q) {
+      const int n = n0 + ncol + 32 * q + 8 * (lane >> 4);
       float v[8];
       take8(acc, q, j, v);
       store8<T>(out + m * p.lddw + n, v, p.d - n, p.vec);
@@ -401,9 +377,9 @@ hipError_t forward(Forward p, hipStream_t stream) {
     return static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   };
   if (const int64_t t = tiles(256, 256); t >= 200)
-    gated_forward_kernel<T, 256, 256, 2, 4><<<static_cast<unsigned>(t), 512, 0, stream>>>(p);
+    gated_forward_kernel<T, 256><<<static_cast<unsigned>(t), 256, 0, stream>>>(p);
   else
-    gated_forward_kernel<T, 128, 128, 2, 2><<<static_cast<unsigned>(tiles(128, 128)), 256, 0, stream>>>(p);
+    gated_forward_kernel<T, 128><<<static_cast<unsigned>(tiles(128, 128)), 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -423,11 +399,11 @@ hipError_t backward(Backward p, hipStream_t stream) {
     p.vec = wide(p.dx, p.lddx);
     if (tiles(p.rows, p.d, 256) >= 200) {
       p.band = std::min(8, p.tiles_m);
-      gated_dx_kernel<T, 256, 256, 2, 4><<<p.tiles_m * p.tiles_n, 512, 0, stream>>>(p);
+      gated_dx_kernel<T, 256><<<p.tiles_m * p.tiles_n, 256, 0, stream>>>(p);
     } else {
       tiles(p.rows, p.d, 128);
       p.band = std::min(8, p.tiles_m);
-      gated_dx_kernel<T, 128, 128, 2, 2><<<p.tiles_m * p.tiles_n, 256, 0, stream>>>(p);
+      gated_dx_kernel<T, 128><<<p.tiles_m * p.tiles_n, 256, 0, stream>>>(p);
     }
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
@@ -436,12 +412,12 @@ hipError_t backward(Backward p, hipStream_t stream) {
     if (2 * tiles(p.f, p.d, 256) >= 200) {
       p.tiles_m *= 2;
       p.band = std::min(8, p.tiles_m);
-      gated_dw_kernel<T, 256, 256, 2, 4><<<p.tiles_m * p.tiles_n, 512, 0, stream>>>(p);
+      gated_dw_kernel<T, 256><<<p.tiles_m * p.tiles_n, 256, 0, stream>>>(p);
     } else {
       tiles(p.f, p.d, 128);
       p.tiles_m *= 2;
       p.band = std::min(8, p.tiles_m);
-      gated_dw_kernel<T, 128, 128, 2, 2><<<p.tiles_m * p.tiles_n, 256, 0, stream>>>(p);
+      gated_dw_kernel<T, 128><<<p.tiles_m * p.tiles_n, 256, 0, stream>>>(p);
     }
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }

@@ -26,6 +26,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <hip/hip_runtime.h>
 
@@ -54,6 +55,10 @@ constexpr uint32_t kOutOfRange = 0x80000000u;   // an offset past every buffer's
 __device__ __forceinline__ constexpr int key(int row) { return (row & 3) | ((row >> 1) & 4); }
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)p));
+}
 
 __device__ __forceinline__ auto buffer(const void* p, int64_t bytes) {
   const int n = static_cast<int>(bytes < 0 ? 0 : (bytes > 0x7fffffff ? 0x7fffffff : bytes));
@@ -87,9 +92,11 @@ struct Loader {
   int64_t limit;          // bytes from base to the end of the operand
   uint32_t voff[kLoads];
   int lds0;               // of this wave's first load
+  __amdgpu_buffer_rsrc_t range;
+  int soff;
 
-  // first: the wave's first load among this operand's
-  __device__ __forceinline__ void init(const char* b, int64_t ld_, int64_t limit_, int64_t cols_left, int wave) {
+  // cols_left (kCols): columns from the tile's first to the operand's last
+  __device__ __forceinline__ void init(const char* b, int64_t ld_, int64_t limit_, int cols_left, int wave) {
     base = b;
     ld = ld_;
     limit = limit_;
@@ -103,31 +110,36 @@ struct Loader {
       voff[j] = static_cast<uint32_t>(row * ld) + chunk * 16;
       if (L == kCols && chunk * 8 >= cols_left) voff[j] = kOutOfRange;
     }
+    range = buffer(base, limit);
+    soff = 0;
   }
-  // loads of step `step` into the LDS tile at `to`; kbytes: length of the contraction in bytes (kRows)
-  __device__ __forceinline__ void issue(char* to, int step, int64_t kbytes) const {
+  // Makes `step` the one that issue() loads.  left (kRows): bytes of k from its
+  // start; where they end inside the step (the last one), its lanes past them are
+  // turned to zeros.
+  __device__ __forceinline__ void at_step(int step, int left) {
     if constexpr (L == kRows) {
-      const auto r = buffer(base, limit);
-      const int soff = step * kStepBytes;
-      const bool whole = soff + kStepBytes <= kbytes;
-      const int lane = threadIdx.x & 63;
+      soff = step * kStepBytes;
+      if (left < kStepBytes) {
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        uint32_t v = voff[j];
-        if (!whole) {
-          const int at = lds0 + j * 1024 + lane * 16;
-          const int chunk = ((at >> 4) & 7) ^ key(at >> 7);
-          if (soff + chunk * 16 >= kbytes) v = kOutOfRange;
+        for (int j = 0; j < kLoads; ++j) {
+          const int at = lds0 + j * 1024 + (threadIdx.x & 63) * 16;
+          if ((((at >> 4) & 7) ^ key(at >> 7)) * 16 >= left) voff[j] = kOutOfRange;
         }
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(to + lds0 + j * 1024), 16, v, soff, 0, 0);
       }
     } else {
       const int64_t skip = static_cast<int64_t>(step) * 64 * ld;
-      const auto r = buffer(base + skip, limit - skip);
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(to + lds0 + j * 1024), 16, voff[j], 0, 0, 0);
+      range = buffer(base + skip, limit - skip);
     }
+  }
+  // Load j of the step into the tile at LDS address `to`.  It returns no register, so
+  // nothing but the waits written in this file has to know of it: in asm, since
+  // after the builtin the compiler waits for it before every transposing read of
+  // the other copy (dx 3.9 ms against 2.4).
+  __device__ __forceinline__ void issue(uint32_t to, int j) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(to + lds0 + j * 1024), "v"(voff[j]), "s"(range), "s"(soff) : "m0");
+#endif
   }
 };
 
@@ -208,6 +220,32 @@ template <>
 __device__ __forceinline__ f32x4 mfma16<Fp16>(i32x4 b, i32x4 a, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
 }
+// x += b0 a and y += b1 a.  In asm, so that the sums stay where they are: with the
+// builtins the compiler moves them between the two halves of the register file
+// inside the loop (210 moves beside 128 matrix instructions).  The nop covers a
+// vector instruction that wrote an operand right before; the sums are read only
+// after settle().
+template <class T>
+__device__ __forceinline__ void mfma_pair(f32x4& x, f32x4& y, const i32x4& b0, const i32x4& b1, const i32x4& a) {
+  if constexpr (std::is_same<T, Bf16>::value)
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %2, %4, %0\n\tv_mfma_f32_16x16x32_bf16 %1, %3, %4, %1"
+                 : "+a"(x), "+a"(y) : "v"(b0), "v"(b1), "v"(a));
+  else
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %2, %4, %0\n\tv_mfma_f32_16x16x32_f16 %1, %3, %4, %1"
+                 : "+a"(x), "+a"(y) : "v"(b0), "v"(b1), "v"(a));
+}
+// Orders the sums behind a wait longer than any of these instructions runs (4
+// passes of 4 cycles): after writing zeros to them, and before reading them.
+template <int MT, int NT>
+__device__ __forceinline__ void settle(f32x4 (&acc)[MT][NT]) {
+  asm volatile("s_nop 7\n\ts_nop 7" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int q = 0; q < NT; ++q) asm volatile("" : "+a"(acc[j][q]));
+  asm volatile("s_nop 7" ::: "memory");
+}
+
 // 128 products of 8-bit values a result; both operands hold the same order of k.
 // FA: the format of A, 0 e4m3, 1 e5m2; B is e4m3.
 template <int FA>
@@ -215,8 +253,118 @@ __device__ __forceinline__ f32x4 mfma8(i32x8 b, i32x8 a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0, 0, 0, 0}, 0, FA, 0, 0, 0, 0);
 }
 
+// Waits until at most LEFT of the wave's loads are under way and its LDS reads
+// have come back, then for the other waves.
+template <int LEFT = 0>
 __device__ __forceinline__ void wait_and_meet() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
+// The steps of one tile of a 16-bit product.  at_step(step) turns both operands'
+// loaders to a step, issue(j, to, i) queues the wave's j-th load of A (i = 0,
+// first in a copy) or B, last(t) finishes the last step's copy before it is read.
+// The wave's rows of A start at `mrow`, its columns at `ncol0` (first half of
+// them) and `ncol1`.  acc[j][q]: matrix tile j of the wave's rows, q of its columns.
+//
+// Half a step (32 k) is in registers while the other half is on its way from
+// LDS, so between two barriers a wave has a whole step of matrix instructions
+// to issue.  The barrier lies in the middle of a step: before it the wave has
+// read all of its copy, after it the next copy is complete and this one free.
+// at_step() is called for two steps past the last one too; their loads are out
+// of range and bring zeros without touching memory, which is cheaper than
+// leaving them out (a second copy of the loop's body).
+template <class T, Layout LA, Layout LB, int BM, int BN, int WM, int WN, class Step, class Issue, class Last>
+__device__ __forceinline__ void multiply(char (*lds)[(BM + BN) * kStepBytes], int first, int steps, int mrow, int ncol0,
+                                         int ncol1, Step&& at_step, Issue&& issue, Last&& last,
+                                         f32x4 (&acc)[BM / WM / 16][BN / WN / 16]) {
+  constexpr int MT = BM / WM / 16, NT = BN / WN / 16, kLoads = BM / 8 / (WM * WN);
+  static_assert(MT == NT && kLoads == MT && BM == BN, "one load of each operand goes with each row of matrix tiles");
+  Reader<LA, BM, MT / 2> ra;
+  Reader<LB, BN, NT / 4> rb[2];
+  ra.init(mrow);
+  rb[0].init(ncol0);
+  rb[1].init(ncol1);
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int q = 0; q < NT; ++q) acc[j][q] = f32x4{0, 0, 0, 0};
+  if (steps <= 0) return;
+  constexpr uint32_t kCopy = (BM + BN) * kStepBytes;
+  const uint32_t copies = lds_address(lds);
+  settle(acc);
+  at_step(first);
+#pragma unroll
+  for (int j = 0; j < 2 * kLoads; ++j) issue(j / 2, copies, j % 2);
+  at_step(first + 1);
+#pragma unroll
+  for (int j = 0; j < 2 * kLoads; ++j) issue(j / 2, copies + kCopy, j % 2);
+  wait_and_meet<2 * kLoads>();
+  if (steps == 1) last(lds[0]);
+  i32x4 a[2][MT], b[2][NT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    a[0][j] = ra.read(lds[0], j, 0);
+    b[0][j] = rb[j / (NT / 2)].read(lds[0] + BM * kStepBytes, j % (NT / 2), 0);
+  }
+  // One row of matrix tiles; between its pairs of matrix instructions (32 cycles
+  // each) fit what prepare(0..NT/2-1) asks for: a single wave issues an
+  // instruction every 4 cycles, so a longer gap would leave the matrix core idle.
+  auto row = [&](int j, int h, auto&& prepare) {
+#pragma unroll
+    for (int q = 0; q < NT; q += 2) {
+      prepare(q / 2);
+      mfma_pair<T>(acc[j][q], acc[j][q + 1], b[h][q], b[h][q + 1], a[h][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Read r of a half step's MT + NT: what its first row of matrix tiles needs comes first.
+  auto read = [&](const char* from, int h, int r) {
+    if (r == 0) a[h][0] = ra.read(from, 0, h);
+    else if (r <= NT) b[h][r - 1] = rb[(r - 1) / (NT / 2)].read(from + BM * kStepBytes, (r - 1) % (NT / 2), h);
+    else a[h][r - NT] = ra.read(from, r - NT, h);
+  };
+  constexpr int kPairs = NT / 2, kReads = MT + NT, kAll = kReads + 2 * kLoads, kEach = kAll / (MT * kPairs);
+  static_assert(kAll == kEach * MT * kPairs && kReads <= MT * kPairs, "what is read and loaded fits between the pairs");
+  for (int s = 0; s < steps; ++s) {
+    const char* t = lds[s & 1];
+    const char* next = lds[(s + 1) & 1];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      row(j, 0, [&](int i) {
+        if (j * kPairs + i < kReads) read(t, 1, j * kPairs + i);
+      });
+    wait_and_meet();
+    if (s + 2 == steps) last(lds[(s + 1) & 1]);
+    at_step(first + s + 2);
+    // the loads first: they have the longest way
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      row(j, 1, [&](int i) {
+#pragma unroll
+        for (int n = 0; n < kEach; ++n) {
+          const int o = (j * kPairs + i) * kEach + n;
+          if (o < 2 * kLoads) issue(o / 2, copies + (s & 1) * kCopy, o % 2);
+          else read(next, 0, o - 2 * kLoads);
+        }
+      });
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load outlives the workgroup's LDS
+  settle(acc);
+}
+
+// m (within the workgroup's tile) of matrix tile j, for this lane.
+__device__ __forceinline__ int row_of(int mrow, int j) {
+  const int lane = threadIdx.x & 63;
+  return mrow + (j >> 1) * 32 + 4 * (j & 1) + 8 * ((lane & 15) >> 2) + (lane & 3);
+}
+// The lane's 8 consecutive columns of a 32-column group.
+template <int MT, int NT>
+__device__ __forceinline__ void take8(const f32x4 (&acc)[MT][NT], int group, int j, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = acc[j][2 * group][i];
+    v[4 + i] = acc[j][2 * group + 1][i];
+  }
 }
 
 // ------------------------------------------------------------- 16-bit results
