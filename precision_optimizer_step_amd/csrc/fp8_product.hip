@@ -8,6 +8,7 @@
 // norm, a hundredth of bf16's rounding and a tenth of fp16's.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "products_internal.h"
 #include "tile_product.h"
@@ -42,9 +43,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
   constexpr int NW = WM * WN;
   constexpr int MT = BM / WM / 16;
   static_assert(BN / WN == 64, "a wave takes 64 columns");
-  static_assert((BM + BN) / 64 <= NW, "a wave loads at most 64 scales a step");
+  static_assert((BM + BN) / 64 == NW, "a wave loads 64 scales a step");
   constexpr int kTile = (BM + BN) * kStepBytes;
-  __shared__ __align__(16) char lds[2][kTile + (BM + BN) * 4];
+  constexpr int kCopy = kTile + (BM + BN) * 4;
+  __shared__ __align__(16) char lds[2][kCopy];
 
   int tm, tn;
   tile_of_group(p.tiles_m, p.tiles_n, p.band, tm, tn);
@@ -61,24 +63,33 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
 
   // this wave's 64 scales: of A's rows (waves 0 .. BM/64 - 1) or of B's
   const bool scales_a = wave < BM / 64;
-  const bool scales = wave < (BM + BN) / 64;
   const int srow = scales_a ? m0 + wave * 64 + lane : n0 + (wave - BM / 64) * 64 + lane;
   const int64_t sstep = scales_a ? p.m : p.nb;
   const char* sbase = reinterpret_cast<const char*>(scales_a ? p.sa : p.sb);
   uint32_t soff = static_cast<uint32_t>((scales_a || !TILE) ? srow : srow / 128) * 4;
   if (srow >= (scales_a ? p.m : p.n)) soff = kOutOfRange;
+  __amdgpu_buffer_rsrc_t srange;
 
-  auto issue = [&](int step) {
-    char* to = lds[step & 1];
+  auto at_step = [&](int step) {
     la.at_step(step, p.k - step * kStepBytes);
     lb.at_step(step, p.k - step * kStepBytes);
-#pragma unroll
-    for (int j = 0; j < BM / 8 / NW; ++j) la.issue(lds_address(to), j);
-#pragma unroll
-    for (int j = 0; j < BN / 8 / NW; ++j) lb.issue(lds_address(to + BM * kStepBytes), j);
-    if (scales)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(sbase + step * sstep * 4, sstep * 4),
-                                               (lds_void*)(to + kTile + wave * 256), 4, soff, 0, 0, 0);
+    srange = buffer(sbase + step * sstep * 4, step < steps ? sstep * 4 : 0);
+  };
+  // the wave's load l of the step: its parts of A, of B, its scales
+  constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW, kAll = kA + kB + 1;
+  const uint32_t copies = lds_address(lds);
+  auto issue = [&](uint32_t to, int l) {
+    if (l < kA) la.issue(to, l);
+    else if (l < kA + kB) lb.issue(to + BM * kStepBytes, l - kA);
+    else load_lds_4(srange, soff, to + kTile + wave * 256);
+  };
+  auto clear = [&](int step) {
+    if (step + 1 == steps && (p.k & 15)) {
+      char* t = lds[step & 1];
+      clear_part_chunk<BM, 64 * NW>(t, p.k - step * kStepBytes);
+      clear_part_chunk<BN, 64 * NW>(t + BM * kStepBytes, p.k - step * kStepBytes);
+      __syncthreads();
+    }
   };
 
   Reader<kRows, BM, MT / 2> ra;
@@ -86,55 +97,103 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
   ra.init(wm * (BM / WM));
   rb.init(wn * 64);
   const int mlane = 8 * ((lane & 15) >> 2) + (lane & 3);
-  f32x4 acc[4][MT];
+  const float* lds_scales = reinterpret_cast<const float*>(lds[0] + kTile);
+  constexpr int kCopyFloats = kCopy / 4;
+  auto both = [](i32x4 lo, i32x4 hi) { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); };
+  f32x4 acc[MT][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int j = 0; j < MT; ++j)
 #pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int q = 0; q < 4; ++q) acc[j][q] = f32x4{0, 0, 0, 0};
 
-  if (steps > 0) issue(0);
-  for (int step = 0; step < steps; ++step) {
-    wait_and_meet();
-    if (step + 1 < steps) issue(step + 1);
-    char* t = lds[step & 1];
-    if (step + 1 == steps && (p.k & 15)) {
-      clear_part_chunk<BM, 64 * NW>(t, p.k - step * kStepBytes);
-      clear_part_chunk<BN, 64 * NW>(t + BM * kStepBytes, p.k - step * kStepBytes);
-      __syncthreads();
-    }
-    const float* sa = reinterpret_cast<const float*>(t + kTile) + wm * (BM / WM);
-    const float* sb = reinterpret_cast<const float*>(t + kTile) + BM + wn * 64;
-    i32x8 b[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const i32x4 lo = rb.read(t + BM * kStepBytes, q, 0), hi = rb.read(t + BM * kStepBytes, q, 1);
-      b[q] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-    f32x4 sn[4];
-    float s1 = 0;
+  // Row j's fragment of A is in a[0] (j even), a[1] (odd) or a[2] (the last).
+  // Before the last two rows everything of this copy has been read: there the
+  // waves meet, the next copy is complete, this one is filled again, and the
+  // next step's B and first row are read.  B alternates between two sets of
+  // registers, so steps go in pairs (a step past the last one adds zeros).
+  i32x8 a[3], b[2][4];
+  float sa[3];
+  auto slot = [](int j) { return j == MT - 1 ? 2 : j & 1; };
+  auto read_a = [&](int step, int j) {
+    const char* t = lds[0] + (step & 1) * kCopy;
+    a[slot(j)] = both(ra.read(t, j, 0), ra.read(t, j, 1));
+    sa[slot(j)] = lds_scales[(step & 1) * kCopyFloats + wm * (BM / WM) + (j >> 1) * 32 + 4 * (j & 1) + mlane];
+  };
+  auto read_b = [&](int step, int set, int q) {
+    const char* t = lds[0] + (step & 1) * kCopy + BM * kStepBytes;
+    b[set][q] = both(rb.read(t, q, 0), rb.read(t, q, 1));
+  };
+  auto run = [&](int step, auto set) {
+    constexpr int S = decltype(set)::value;
+    const float* sb = lds_scales + (step & 1) * kCopyFloats + BM + wn * 64;
+    f32x4 sn[TILE ? 1 : 4];
     if constexpr (TILE) {
-      s1 = sb[0];
+      sn[0][0] = sb[0];
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         sn[q] = *reinterpret_cast<const f32x4*>(sb + (q >> 1) * 32 + 8 * (lane >> 4) + 4 * (q & 1));
     }
+    // A part is added two matrix instructions after its own: next to it the
+    // hardware's wait for its result (about 10 instructions) would be spent idle.
+    f32x4 part[3];
+    float s[2] = {0.0f, 0.0f};
+    auto add = [&](int k) {
+      const int j = k / 4, q = k % 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[j][q][i] = __builtin_fmaf(part[k % 3][i], TILE ? s[j & 1] : s[j & 1] * sn[TILE ? 0 : q][i], acc[j][q][i]);
+      asm volatile("" : "+v"(acc[j][q]));   // here and not later: 64 parts would not fit the registers
+    };
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-      const i32x4 lo = ra.read(t, j, 0), hi = ra.read(t, j, 1);
-      const i32x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      float s = sa[(j >> 1) * 32 + 4 * (j & 1) + mlane];
-      if constexpr (TILE) s *= s1;
+      if (j == MT - 2) {
+        wait_and_meet();
+        clear(step + 1);
+        at_step(step + 2);
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f32x4 part = mfma8<FA>(b[q], a);
+        if (j < MT - 2) {
+          if (q == 0) read_a(step, j + 1);
+          if (q == 2 && j == MT - 3) read_a(step, MT - 1);
+        } else {
+          // the last two rows: 8 places for the loads, B and the next first row
+          const int at = (j - (MT - 2)) * 4 + q;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float w = TILE ? s : s * sn[q][i];
-          acc[q][j][i] = __builtin_fmaf(part[i], w, acc[q][j][i]);
+          for (int l = 0; l < kAll; ++l)
+            if (l * 6 / kAll == at) issue(copies + (step & 1) * kCopy, l);
+          if (at >= 2 && at < 6) read_b(step + 1, 1 - S, at - 2);
+          if (at == 6) read_a(step + 1, 0);
         }
+        const int k = 4 * j + q;
+        part[k % 3] = mfma8<FA>(b[S][q], a[slot(j)]);
+        if (k >= 2) add(k - 2);
+        if (q == 1) s[j & 1] = TILE ? sa[slot(j)] * sn[0][0] : sa[slot(j)];
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+    add(4 * MT - 2);
+    add(4 * MT - 1);
+  };
+
+  if (steps > 0) {
+    at_step(0);
+#pragma unroll
+    for (int l = 0; l < kAll; ++l) issue(copies, l);
+    at_step(1);
+#pragma unroll
+    for (int l = 0; l < kAll; ++l) issue(copies + kCopy, l);
+    wait_and_meet<kAll>();
+    clear(0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) read_b(0, 0, q);
+    read_a(0, 0);
+    for (int step = 0; step < steps; step += 2) {
+      run(step, std::integral_constant<int, 0>{});
+      run(step + 1, std::integral_constant<int, 1>{});
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load outlives the workgroup's LDS
   }
 
 #pragma unroll
@@ -147,8 +206,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
       float v[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = acc[2 * q][j][i];
-        v[4 + i] = acc[2 * q + 1][j][i];
+        v[i] = acc[j][2 * q][i];
+        v[4 + i] = acc[j][2 * q + 1][i];
       }
       store8<C>(p.c + m * p.ldc + n, v, p.n - n, p.vec);
     }

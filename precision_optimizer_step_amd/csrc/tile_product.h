@@ -80,6 +80,13 @@ __device__ __forceinline__ void tile_of_group(int tiles_m, int tiles_n, int band
   tn = in / h;
 }
 
+// One wave load of 4 bytes a lane into LDS at `to`; as Loader::issue, in asm.
+__device__ __forceinline__ void load_lds_4(__amdgpu_buffer_rsrc_t range, uint32_t off, uint32_t to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(range));
+#endif
+}
+
 // One operand's tile loads.  SIZE rows (or columns) of the tile, NW waves.
 template <Layout L, int SIZE, int NW>
 struct Loader {
@@ -134,11 +141,12 @@ struct Loader {
   // Load j of the step into the tile at LDS address `to`.  It returns no register, so
   // nothing but the waits written in this file has to know of it: in asm, since
   // after the builtin the compiler waits for it before every transposing read of
-  // the other copy (dx 3.9 ms against 2.4).
+  // the other copy (dx 3.9 ms against 2.4).  (m0, which it writes, is a reserved
+  // register: the compiler keeps nothing in it and no other instruction here reads it.)
   __device__ __forceinline__ void issue(uint32_t to, int j) const {
 #if defined(__HIP_DEVICE_COMPILE__)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(to + lds0 + j * 1024), "v"(voff[j]), "s"(range), "s"(soff) : "m0");
+                 :: "s"(to + lds0 + j * 1024), "v"(voff[j]), "s"(range), "s"(soff));
 #endif
   }
 };
