@@ -37,8 +37,12 @@ struct Product {
 // One BM x BN tile of C, WM x WN waves.  The scales of a step's block of k lie
 // in LDS beside its operand tiles, one for each row of either (TILE scales are
 // spread over their rows by the loads' addresses).
-template <int FA, class C, bool TILE, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product p) {
+//
+// KG > 1: KG teams of WM x WN waves share the tile's steps in turn, each with its
+// own copies, and add their sums through LDS at the end, in a fixed order: for
+// results too small to give every CU a tile.
+template <int FA, class C, bool TILE, int BM, int BN, int WM, int WN, int KG = 1>
+__global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = WM * WN;
   constexpr int MT = BM / WM / 16;
@@ -46,11 +50,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
   static_assert((BM + BN) / 64 == NW, "a wave loads 64 scales a step");
   constexpr int kTile = (BM + BN) * kStepBytes;
   constexpr int kCopy = kTile + (BM + BN) * 4;
-  __shared__ __align__(16) char lds[2][kCopy];
+  __shared__ __align__(16) char lds_all[KG][2][kCopy];
 
   int tm, tn;
   tile_of_group(p.tiles_m, p.tiles_n, p.band, tm, tn);
-  const int wave = wave_id(), lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63;
+  const int team = KG > 1 ? wave_id() / NW : 0, wave = KG > 1 ? wave_id() % NW : wave_id();
+  char(*lds)[kCopy] = lds_all[team];
   const int wm = wave / WN, wn = wave % WN;
   const int m0 = tm * BM, n0 = tn * BN;
   const int64_t kbytes = p.k, kround = (kbytes + 15) & ~int64_t{15};
@@ -59,7 +65,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
   Loader<kRows, BN, NW> lb;
   la.init(p.a + m0 * p.lda, p.lda, (std::min(BM, p.m - m0) - 1) * p.lda + kround, 0, wave);
   lb.init(p.b + n0 * p.ldb, p.ldb, (std::min(BN, p.n - n0) - 1) * p.ldb + kround, 0, wave);
-  const int steps = (p.k + kStepBytes - 1) / kStepBytes;
+  const int all_steps = (p.k + kStepBytes - 1) / kStepBytes;
+  const int steps = (all_steps + KG - 1) / KG;     // of each team: step s is s*KG + team of the product
 
   // this wave's 64 scales: of A's rows (waves 0 .. BM/64 - 1) or of B's
   const bool scales_a = wave < BM / 64;
@@ -70,10 +77,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
   if (srow >= (scales_a ? p.m : p.n)) soff = kOutOfRange;
   __amdgpu_buffer_rsrc_t srange;
 
-  auto at_step = [&](int step) {
+  auto at_step = [&](int s) {
+    const int step = s * KG + team;
     la.at_step(step, p.k - step * kStepBytes);
     lb.at_step(step, p.k - step * kStepBytes);
-    srange = buffer(sbase + step * sstep * 4, step < steps ? sstep * 4 : 0);
+    srange = buffer(sbase + step * sstep * 4, step < all_steps ? sstep * 4 : 0);
   };
   // the wave's load l of the step: its parts of A, of B, its scales
   constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW, kAll = kA + kB + 1;
@@ -85,9 +93,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
   };
   auto clear = [&](int step) {
     if (step + 1 == steps && (p.k & 15)) {
-      char* t = lds[step & 1];
-      clear_part_chunk<BM, 64 * NW>(t, p.k - step * kStepBytes);
-      clear_part_chunk<BN, 64 * NW>(t + BM * kStepBytes, p.k - step * kStepBytes);
+      if (KG == 1 || step * KG + team + 1 == all_steps)
+        clear_part_chunk<BM + BN, 64 * NW>(lds[step & 1], p.k - (all_steps - 1) * kStepBytes, threadIdx.x - team * 64 * NW);
       __syncthreads();
     }
   };
@@ -154,7 +161,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (j < MT - 2) {
+        constexpr bool two = MT == 2;     // both rows are read at the end of the step before
+        if (!two && j < MT - 2) {
           if (q == 0) read_a(step, j + 1);
           if (q == 2 && j == MT - 3) read_a(step, MT - 1);
         } else {
@@ -164,7 +172,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
           for (int l = 0; l < kAll; ++l)
             if (l * 6 / kAll == at) issue(copies + (step & 1) * kCopy, l);
           if (at >= 2 && at < 6) read_b(step + 1, 1 - S, at - 2);
-          if (at == 6) read_a(step + 1, 0);
+          if (!two && at == 6) read_a(step + 1, 0);
         }
         const int k = 4 * j + q;
         part[k % 3] = mfma8<FA>(b[S][q], a[slot(j)]);
@@ -172,6 +180,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
         if (q == 1) s[j & 1] = TILE ? sa[slot(j)] * sn[0][0] : sa[slot(j)];
         __builtin_amdgcn_sched_barrier(0);
       }
+    }
+    if constexpr (MT == 2) {
+      read_a(step + 1, 0);
+      read_a(step + 1, 1);
     }
     add(4 * MT - 2);
     add(4 * MT - 1);
@@ -189,6 +201,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
 #pragma unroll
     for (int q = 0; q < 4; ++q) read_b(0, 0, q);
     read_a(0, 0);
+    if constexpr (MT == 2) read_a(0, 1);
     for (int step = 0; step < steps; step += 2) {
       run(step, std::integral_constant<int, 0>{});
       run(step + 1, std::integral_constant<int, 1>{});
@@ -196,12 +209,29 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load outlives the workgroup's LDS
   }
 
+  if constexpr (KG > 1) {
+    // every team's sums, [team][wave][matrix tile][lane]; each then finishes its share of the 32-column groups
+    f32x4* sums = reinterpret_cast<f32x4*>(lds_all);
+    static_assert(sizeof(lds_all) >= KG * NW * MT * 4 * 64 * sizeof(f32x4), "");
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 4 * MT; ++t) sums[((team * NW + wave) * 4 * MT + t) * 64 + lane] = acc[t / 4][t % 4];
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 4 * MT; ++t) {
+      f32x4 v = sums[(wave * 4 * MT + t) * 64 + lane];
+#pragma unroll
+      for (int g = 1; g < KG; ++g) v += sums[((g * NW + wave) * 4 * MT + t) * 64 + lane];
+      acc[t / 4][t % 4] = v;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const int m = m0 + wm * (BM / WM) + (j >> 1) * 32 + 4 * (j & 1) + mlane;
     if (m >= p.m) continue;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
+      if (KG > 1 && (2 * j + q) % KG != team) continue;
       const int n = n0 + wn * 64 + q * 32 + 8 * (lane >> 4);
       float v[8];
 #pragma unroll
@@ -215,18 +245,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(const Product 
 #endif
 }
 
-// Few rows (one token to a short prompt): the time is that of reading B, so
-// nothing goes through LDS.  A workgroup owns 16 n and 16*MT m; its 4 waves
-// take every fourth block of k, hold B's and A's fragments in registers straight
-// from memory (a lane 32 bytes of a row's 128) and add their sums through LDS
-// at the end, in a fixed order.
-template <class V>
-__device__ __forceinline__ V load_k(const char* row, int at, int k) {
-  static_assert(sizeof(V) == 16, "");
-  if (at + 16 <= k) return *reinterpret_cast<const V*>(row + at);
-  V v = V{0, 0, 0, 0};
-  if (at < k) {
-    v = *reinterpret_cast<const V*>(row + at);
+// At most 16 rows (single tokens): the time is that of reading B, so nothing goes
+// through LDS.  A workgroup owns 16 n; each of its 4 waves takes a quarter of k,
+// in one piece, holds B's and A's fragments in registers straight from memory (a
+// lane 32 bytes of a row's 128, four blocks under way at once) and adds its sums
+// to the others' through LDS at the end, in a fixed order.  One row, n = 4096, k
+// = 16384: 12.5 us, 5.4 TB/s.  Waves that take blocks in turn instead read all
+// rows at one place of k at a time; where rows lie a power of two apart that
+// is one memory channel: 21 us.
+__device__ __forceinline__ i32x4 load_part(const char* row, int at, int k) {
+  i32x4 v = i32x4{0, 0, 0, 0};
+  if (at < k) v = *reinterpret_cast<const i32x4*>(row + at);
+  if (at + 16 > k) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const int b = k - at - 4 * w;
@@ -237,85 +267,131 @@ __device__ __forceinline__ V load_k(const char* row, int at, int k) {
   return v;
 }
 
-template <int FA, class C, bool TILE, int MT>
+template <int FA, class C, bool TILE>
 __global__ __launch_bounds__(256) void product_few_kernel(const Product p) {
-  __shared__ __align__(16) f32x4 sums[4][MT][64];
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int kDepth = 4, kScales = TILE ? 1 : 4;
+  __shared__ __align__(16) f32x4 sums[4][64];
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT;
-  const int brow = std::min(n0 + r, p.n - 1);
-  const char* b = p.b + brow * p.ldb;
-  const char* a[MT];
-  int am[MT];
+  const int n0 = blockIdx.x * 16;
+  const int am = std::min(r, p.m - 1);
+  const char* b = p.b + std::min(n0 + r, p.n - 1) * p.ldb + g * 32;
+  const char* a = p.a + am * p.lda + g * 32;
+  int bn[kScales];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    am[j] = std::min(m0 + 16 * j + r, p.m - 1);
-    a[j] = p.a + am[j] * p.lda;
+  for (int i = 0; i < kScales; ++i) bn[i] = TILE ? n0 / 128 : std::min(n0 + 4 * g + i, p.n - 1);
+  f32x4 acc = f32x4{0, 0, 0, 0};
+
+  struct Block {
+    i32x8 b, a;
+    float sa, sb[kScales];
+  };
+  auto scales = [&](Block& x, int step) {
+#pragma unroll
+    for (int i = 0; i < kScales; ++i) x.sb[i] = p.sb[static_cast<int64_t>(step) * p.nb + bn[i]];
+    x.sa = p.sa[static_cast<int64_t>(step) * p.m + am];
+  };
+  auto both = [](i32x4 lo, i32x4 hi) { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); };
+  auto whole = [&](const char* row, int step) {
+    const i32x4* v = reinterpret_cast<const i32x4*>(row + step * kStepBytes);
+    return both(v[0], v[1]);
+  };
+  auto load = [&](Block& x, int step) {
+    x.b = whole(b, step);
+    x.a = whole(a, step);
+    scales(x, step);
+  };
+  auto add = [&](const Block& x) {
+    const f32x4 part = mfma8<FA>(x.b, x.a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(part[i], x.sa * x.sb[TILE ? 0 : i], acc[i]);
+  };
+  const int steps = p.k / kStepBytes;      // whole blocks
+  int step = steps * wave / 4;
+  const int end = steps * (wave + 1) / 4;
+  for (; step + kDepth <= end; step += kDepth) {
+    Block x[kDepth];
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) load(x[i], step + i);
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) add(x[i]);
   }
-  f32x4 acc[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) acc[j] = f32x4{0, 0, 0, 0};
-  const int steps = (p.k + kStepBytes - 1) / kStepBytes;
-#pragma unroll 4
-  for (int step = wave; step < steps; step += 4) {
-    const int at = step * kStepBytes + g * 32;
-    const i32x4 b0 = load_k<i32x4>(b, at, p.k), b1 = load_k<i32x4>(b, at + 16, p.k);
-    const i32x8 bv = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
-    float sn[4];
-    if constexpr (TILE) {
-      sn[0] = p.sb[static_cast<int64_t>(step) * p.nb + n0 / 128];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sn[i] = p.sb[static_cast<int64_t>(step) * p.nb + std::min(n0 + 4 * g + i, p.n - 1)];
-    }
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const i32x4 a0 = load_k<i32x4>(a[j], at, p.k), a1 = load_k<i32x4>(a[j], at + 16, p.k);
-      const i32x8 av = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
-      const float s = p.sa[static_cast<int64_t>(step) * p.m + am[j]];
-      const f32x4 part = mfma8<FA>(bv, av);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = __builtin_fmaf(part[i], s * sn[TILE ? 0 : i], acc[j][i]);
-    }
+  for (; step < end; ++step) {
+    Block x;
+    load(x, step);
+    add(x);
   }
-#pragma unroll
-  for (int j = 0; j < MT; ++j) sums[wave][j][lane] = acc[j];
+  if (wave == 3 && p.k % kStepBytes) {
+    const int left = p.k % kStepBytes - g * 32;
+    Block x;
+    auto part = [&](const char* row) {
+      return both(load_part(row + steps * kStepBytes, 0, left), load_part(row + steps * kStepBytes, 16, left));
+    };
+    x.b = part(b);
+    x.a = part(a);
+    scales(x, steps);
+    add(x);
+  }
+  sums[wave][lane] = acc;
   __syncthreads();
-  // lane l of wave w finishes m tile w (of MT)
-  for (int j = wave; j < MT; j += 4) {
-    const f32x4 t = (sums[0][j][lane] + sums[1][j][lane]) + (sums[2][j][lane] + sums[3][j][lane]);
-    const int m = m0 + 16 * j + r;
-    if (m >= p.m) continue;
+  if (wave == 0 && r < p.m) {
+    const f32x4 t = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int n = n0 + 4 * g + i;
-      if (n >= p.n) continue;
-      p.c[m * p.ldc + n] = static_cast<uint16_t>(bits_of(C{}, t[i]));
+      if (n < p.n) p.c[r * p.ldc + n] = static_cast<uint16_t>(bits_of(C{}, t[i]));
     }
   }
+#endif
 }
 
+// Microseconds of one step (128 k) of a whole launch of `tiles` tiles, of which
+// `at_once` run side by side on the chip (256 CUs) and a part of at most `few` in
+// less time: `round` a full round takes, `short_round` such a part.
+double rounds(int64_t tiles, int at_once, double round, int few, double short_round) {
+  const int64_t rest = tiles % at_once;
+  return static_cast<double>(tiles / at_once) * round + (rest == 0 ? 0.0 : rest <= few ? short_round : round);
+}
+
+// The kernel is the one that the estimate below calls fastest.  Its constants
+// were measured at k = 4096 (us a step, n = 4096 unless named; TILE, and ROW
+// where it differs; the kernels from left to right):
+//              256x256    128x128   128x128, 2 teams   64x64, 2 teams   64x64, 4 teams
+//   m =  128     1.45       0.64          0.59              0.34             0.32
+//   m =  512     1.54       0.77          0.66              0.52             0.70
+//   m = 1024     1.57       0.83          0.74              0.97             1.38
+//   m = 2048     1.66       1.15          1.45              1.83             2.66
+//   m = 4096     1.96/2.36  2.19/2.50     2.74              3.57             5.12
+//   8192^2       7.7/9.6    8.8/10.2      10.9              14.2             20.3
+// At most 16 rows go to the kernel without LDS (k = 16384, one row: 12.5 us
+// against 30.5 of the 64x64 tiles; 16 rows: 17.3 against 31.0; but n = 16384, k =
+// 4096, 16 rows: 16.7 against 14.9).
 template <int FA, class C, bool TILE>
 hipError_t launch(Product p, hipStream_t stream) {
-  if (p.m <= 64) {
-    const dim3 grid((p.n + 15) / 16, 1);
-    if (p.m <= 16) product_few_kernel<FA, C, TILE, 1><<<grid, 256, 0, stream>>>(p);
-    else if (p.m <= 32) product_few_kernel<FA, C, TILE, 2><<<grid, 256, 0, stream>>>(p);
-    else product_few_kernel<FA, C, TILE, 4><<<grid, 256, 0, stream>>>(p);
+  if (p.m <= 16) {
+    product_few_kernel<FA, C, TILE><<<(p.n + 15) / 16, 256, 0, stream>>>(p);
     return hipGetLastError();
   }
-  auto tiles = [&](int bm, int bn) {
-    p.tiles_m = (p.m + bm - 1) / bm;
-    p.tiles_n = (p.n + bn - 1) / bn;
-    p.band = std::min(8, p.tiles_m);
-    return static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  auto tiles = [&](int size) { return static_cast<int64_t>((p.m + size - 1) / size) * ((p.n + size - 1) / size); };
+  const double cost[5] = {
+      rounds(tiles(256), 256, TILE ? 2.0 : 2.4, 0, 0),
+      rounds(tiles(128), 512, TILE ? 1.12 : 1.26, 256, 0.80),
+      rounds(tiles(128), 256, 0.72, 0, 0),
+      rounds(tiles(64), 512, 0.53, 256, 0.34),
+      rounds(tiles(64), 256, 0.31, 0, 0),
   };
-  if (tiles(256, 256) >= 200) {
-    product_kernel<FA, C, TILE, 256, 256, 2, 4><<<p.tiles_m * p.tiles_n, 512, 0, stream>>>(p);
-  } else {
-    const int64_t t = tiles(128, 128);
-    product_kernel<FA, C, TILE, 128, 128, 2, 2><<<static_cast<unsigned>(t), 256, 0, stream>>>(p);
-  }
+  const int best = static_cast<int>(std::min_element(cost, cost + 5) - cost);
+  const int size = best == 0 ? 256 : best < 3 ? 128 : 64;
+  p.tiles_m = (p.m + size - 1) / size;
+  p.tiles_n = (p.n + size - 1) / size;
+  p.band = std::min(8, p.tiles_m);
+  const unsigned grid = static_cast<unsigned>(tiles(size));
+  if (best == 0) product_kernel<FA, C, TILE, 256, 256, 2, 4><<<grid, 512, 0, stream>>>(p);
+  else if (best == 1) product_kernel<FA, C, TILE, 128, 128, 2, 2><<<grid, 256, 0, stream>>>(p);
+  else if (best == 2) product_kernel<FA, C, TILE, 128, 128, 2, 2, 2><<<grid, 512, 0, stream>>>(p);
+  else if (best == 3) product_kernel<FA, C, TILE, 64, 64, 2, 1, 2><<<grid, 256, 0, stream>>>(p);
+  else product_kernel<FA, C, TILE, 64, 64, 2, 1, 4><<<grid, 512, 0, stream>>>(p);
   return hipGetLastError();
 }
 

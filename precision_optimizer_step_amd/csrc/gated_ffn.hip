@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void gated_forward_kernel(co
   const int steps = static_cast<int>((kbytes + kStepBytes - 1) / kStepBytes);
   auto last = [&](char* t) {
     if (kbytes & 15) {
-      clear_part_chunk<2 * B, 256>(t, static_cast<int>(kbytes - (steps - 1) * kStepBytes));
+      clear_part_chunk<2 * B, 256>(t, static_cast<int>(kbytes - (steps - 1) * kStepBytes), threadIdx.x);
       __syncthreads();
     }
   };

@@ -154,9 +154,9 @@ struct Loader {
 // Clears the bytes of k at and past `kbytes` in the one 16-byte chunk of each
 // row that holds both kinds (an operand whose k does not end on 16 bytes).
 template <int ROWS, int THREADS>
-__device__ __forceinline__ void clear_part_chunk(char* t, int kbytes_in_step) {
+__device__ __forceinline__ void clear_part_chunk(char* t, int kbytes_in_step, int thread) {
   const int chunk = kbytes_in_step >> 4, keep = kbytes_in_step & 15;
-  for (int row = threadIdx.x; row < ROWS; row += THREADS) {
+  for (int row = thread; row < ROWS; row += THREADS) {
     uint32_t* p = reinterpret_cast<uint32_t*>(t + row * kStepBytes + ((chunk ^ key(row)) << 4));
 #pragma unroll
     for (int w = 0; w < 4; ++w) {

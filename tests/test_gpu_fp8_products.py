@@ -205,6 +205,16 @@ def test_product_largest_tiles(a_kind, tile, k):
     check_exact(3601, 3610, k, a_kind=a_kind, tile=tile, seed=8)
 
 
+@pytest.mark.parametrize("a_kind", [E4, E5])
+@pytest.mark.parametrize("tile", [True, False])
+@pytest.mark.parametrize("m,n", [(2001, 4090), (1001, 4090), (501, 4090), (130, 4090)])
+def test_product_every_tile_size(a_kind, tile, m, n):
+    """128 x 128 with one team of waves and with two, 64 x 64 with two and with four; each at
+    depths that give the teams different numbers of steps, and none to some."""
+    for k in (100, 300, 520, 1153):
+        check_exact(m, n, k, a_kind=a_kind, tile=tile, seed=k)
+
+
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float16])
 def test_product_result_strides(out):
     for ldc_extra in (0, 1, 3, 8):
