@@ -209,22 +209,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Pro
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load outlives the workgroup's LDS
   }
 
-  if constexpr (KG > 1) {
-    // every team's sums, [team][wave][matrix tile][lane]; each then finishes its share of the 32-column groups
-    f32x4* sums = reinterpret_cast<f32x4*>(lds_all);
-    static_assert(sizeof(lds_all) >= KG * NW * MT * 4 * 64 * sizeof(f32x4), "");
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < 4 * MT; ++t) sums[((team * NW + wave) * 4 * MT + t) * 64 + lane] = acc[t / 4][t % 4];
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < 4 * MT; ++t) {
-      f32x4 v = sums[(wave * 4 * MT + t) * 64 + lane];
-#pragma unroll
-      for (int g = 1; g < KG; ++g) v += sums[((g * NW + wave) * 4 * MT + t) * 64 + lane];
-      acc[t / 4][t % 4] = v;
-    }
-  }
+  // each team finishes its share of the 32-column groups
+  add_teams<KG, NW, MT, 4>(lds_all, team, wave, acc);
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const int m = m0 + wm * (BM / WM) + (j >> 1) * 32 + 4 * (j & 1) + mlane;
@@ -234,11 +220,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Pro
       if (KG > 1 && (2 * j + q) % KG != team) continue;
       const int n = n0 + wn * 64 + q * 32 + 8 * (lane >> 4);
       float v[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = acc[j][2 * q][i];
-        v[4 + i] = acc[j][2 * q + 1][i];
-      }
+      take8(acc, q, j, v);
       store8<C>(p.c + m * p.ldc + n, v, p.n - n, p.vec);
     }
   }

@@ -72,53 +72,58 @@ struct Forward {
 // A tile holds B/2 rows of Wg and the same rows of Wu beside B rows of x; a
 // wave takes as many columns of one as of the other, so g and u of one h meet
 // in one lane.
-template <class T, int B>
-__global__ __launch_bounds__(256, B == 256 ? 1 : 2) void gated_forward_kernel(const Forward p) {
+template <class T, class G>
+__global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_forward_kernel(const Forward p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int T16 = B / 32, HALF = B / 2;
-  __shared__ __align__(16) char lds[2][2 * B * kStepBytes];
+  constexpr int S = G::kSize, KG = G::kTeams, HALF = S / 2;
+  __shared__ __align__(16) typename G::Lds lds;
   int tm, tn;
   tile_of_group(p.tiles_m, p.tiles_n, p.band, tm, tn);
-  const int wave = wave_id(), lane = threadIdx.x & 63;
-  const int mrow = (wave >> 1) * HALF, ncol = (wave & 1) * (HALF / 2);
-  const int m0 = tm * B, f0 = tn * HALF;
-  const int64_t kbytes = 2 * int64_t{p.d}, kround = (kbytes + 15) & ~int64_t{15};
-  Loader<kRows, B, 4> la;
-  Loader<kRows, HALF, 2> lb;
-  la.init(p.x + m0 * p.ldx, p.ldx, (std::min(B, p.rows - m0) - 1) * p.ldx + kround, 0, wave);
-  const bool second = wave >= 2;
-  lb.init((second ? p.wu : p.wg) + f0 * p.ldw, p.ldw, (std::min(HALF, p.f - f0) - 1) * p.ldw + kround, 0, wave & 1);
-  const int bto = (B + (second ? HALF : 0)) * kStepBytes;
-  auto at_step = [&](int step) {
-    const int left = static_cast<int>(kbytes) - step * kStepBytes;
-    la.at_step(step, left);
-    lb.at_step(step, left);
+  const int lane = threadIdx.x & 63, team = wave_id() / G::NW, wave = wave_id() % G::NW;
+  const int mrow = wave / G::WN * (S / G::WM), ncol = wave % G::WN * (HALF / G::WN);
+  const int m0 = tm * S, f0 = tn * HALF;
+  const int kbytes = 2 * p.d;
+  const int64_t kround = (kbytes + 15) & ~15;
+  Loader<kRows, S, G::NW> la;
+  Loader<kRows, HALF, G::NW / 2> lb;
+  la.init(p.x + m0 * p.ldx, p.ldx, (std::min(S, p.rows - m0) - 1) * p.ldx + kround, 0, wave);
+  const bool second = wave >= G::NW / 2;
+  lb.init((second ? p.wu : p.wg) + f0 * p.ldw, p.ldw, (std::min(HALF, p.f - f0) - 1) * p.ldw + kround, 0,
+          second ? wave - G::NW / 2 : wave);
+  const int bto = (S + (second ? HALF : 0)) * kStepBytes;
+  const int all_steps = (kbytes + kStepBytes - 1) / kStepBytes, steps = (all_steps + KG - 1) / KG;
+  auto at_step = [&](int s) {
+    const int step = s * KG + team;
+    la.at_step(step, kbytes - step * kStepBytes);
+    lb.at_step(step, kbytes - step * kStepBytes);
   };
   auto issue = [&](int j, uint32_t to, int i) {
     if (i == 0) la.issue(to, j);
     else lb.issue(to + bto, j);
   };
-  const int steps = static_cast<int>((kbytes + kStepBytes - 1) / kStepBytes);
   auto last = [&](char* t) {
     if (kbytes & 15) {
-      clear_part_chunk<2 * B, 256>(t, static_cast<int>(kbytes - (steps - 1) * kStepBytes), threadIdx.x);
+      if (KG == 1 || (steps - 1) * KG + team + 1 == all_steps)
+        clear_part_chunk<2 * S, 64 * G::NW>(t, kbytes - (all_steps - 1) * kStepBytes, threadIdx.x - team * 64 * G::NW);
       __syncthreads();
     }
   };
-  f32x4 acc[T16][T16];
-  multiply<T, kRows, kRows, B, B, 2, 2>(lds, 0, steps, mrow, ncol, HALF + ncol, at_step, issue, last, acc);
+  f32x4 acc[G::MT][G::NT];
+  multiply<T, G, kRows, kRows>(lds[team], steps, mrow, ncol, HALF + ncol, at_step, issue, last, acc);
+  add_teams<KG, G::NW>(lds, team, wave, acc);
 
   with_act(p.act, [&](auto act) {
 #pragma unroll
-    for (int j = 0; j < T16; ++j) {
+    for (int j = 0; j < G::MT; ++j) {
       const int64_t m = m0 + row_of(mrow, j);
       if (m >= p.rows) continue;
 #pragma unroll
-      for (int q = 0; q < T16 / 4; ++q) {
+      for (int q = 0; q < G::NT / 4; ++q) {
+        if (KG > 1 && (j * (G::NT / 4) + q) % KG != team) continue;    // each team its share
         const int n = f0 + ncol + 32 * q + 8 * (lane >> 4);
         float g[8], u[8], h[8];
         take8(acc, q, j, g);
-        take8(acc, q + T16 / 4, j, u);
+        take8(acc, q + G::NT / 4, j, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = activate<decltype(act)::value>(g[i]) * u[i];
         store8<T>(p.h + m * p.ldh + n, h, p.f - n, p.vec);
@@ -132,67 +137,85 @@ __global__ __launch_bounds__(256, B == 256 ? 1 : 2) void gated_forward_kernel(co
 #endif
 }
 
-// Few rows: the time is that of reading both weights.  A workgroup owns 16
-// columns of h; its 4 waves take every fourth 64 of k straight from memory and
-// add their sums through LDS in a fixed order.
-__device__ __forceinline__ i32x4 load_part(const char* row, int64_t at, int64_t bytes) {
-  if (at + 16 <= bytes) return *reinterpret_cast<const i32x4*>(row + at);
+// At most 16 rows (single tokens): the time is that of reading both weights, so
+// nothing goes through LDS.  A workgroup owns 16 columns of h; each of its 4
+// waves takes a quarter of k, in one piece (waves in turn would read all rows at
+// one place of k at a time: where rows lie a power of two apart that is one memory
+// channel), and adds its sums to the others' in a fixed order.
+__device__ __forceinline__ i32x4 load_part(const char* row, int at, int bytes) {
   i32x4 v = i32x4{0, 0, 0, 0};
-  if (at < bytes) {
-    v = *reinterpret_cast<const i32x4*>(row + at);
-    const int n = static_cast<int>(bytes - at);   // even
+  if (at < bytes) v = *reinterpret_cast<const i32x4*>(row + at);
+  if (at + 16 > bytes) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      if (n - 4 * w <= 0) v[w] = 0;
-      else if (n - 4 * w < 4) v[w] &= 0xffff;
+      const int n = bytes - at - 4 * w;      // even
+      if (n <= 0) v[w] = 0;
+      else if (n < 4) v[w] &= 0xffff;
     }
   }
   return v;
 }
 
-template <class T, int MT>
+template <class T>
 __global__ __launch_bounds__(256) void gated_forward_few_kernel(const Forward p) {
-  __shared__ __align__(16) f32x4 sums[4][2][MT][64];
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int kDepth = 4;
+  __shared__ __align__(16) f32x4 sums[4][2][64];
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16;
-  const int64_t row = std::min(n0 + r, p.f - 1), bytes = 2 * int64_t{p.d};
-  const char* wg = p.wg + row * p.ldw;
-  const char* wu = p.wu + row * p.ldw;
-  const char* x[MT];
+  const int n0 = blockIdx.x * 16, bytes = 2 * p.d;
+  const int64_t row = std::min(n0 + r, p.f - 1);
+  const char* from[3] = {p.wg + row * p.ldw + g * 32, p.wu + row * p.ldw + g * 32,
+                         p.x + std::min(r, p.rows - 1) * p.ldx + g * 32};
+  f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+  struct Part {
+    i32x4 v[3][2];
+  };
+  auto load = [&](Part& x, int step) {
 #pragma unroll
-  for (int j = 0; j < MT; ++j) x[j] = p.x + std::min(16 * j + r, p.rows - 1) * p.ldx;
-  f32x4 acc[2][MT];
+    for (int i = 0; i < 3; ++i)
 #pragma unroll
-  for (int j = 0; j < MT; ++j) acc[0][j] = acc[1][j] = f32x4{0, 0, 0, 0};
-  const int steps = static_cast<int>((bytes + kStepBytes - 1) / kStepBytes);
-#pragma unroll 4
-  for (int step = wave; step < steps; step += 4) {
-    const int64_t at = int64_t{step} * kStepBytes + g * 32;
+      for (int h = 0; h < 2; ++h) x.v[i][h] = *reinterpret_cast<const i32x4*>(from[i] + step * kStepBytes + 16 * h);
+  };
+  auto add = [&](const Part& x) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const i32x4 bg = load_part(wg, at + 16 * h, bytes), bu = load_part(wu, at + 16 * h, bytes);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const i32x4 a = load_part(x[j], at + 16 * h, bytes);
-        acc[0][j] = mfma16<T>(bg, a, acc[0][j]);
-        acc[1][j] = mfma16<T>(bu, a, acc[1][j]);
-      }
+      acc[0] = mfma16<T>(x.v[0][h], x.v[2][h], acc[0]);
+      acc[1] = mfma16<T>(x.v[1][h], x.v[2][h], acc[1]);
     }
-  }
+  };
+  const int steps = bytes / kStepBytes;
+  int step = steps * wave / 4;
+  const int end = steps * (wave + 1) / 4;
+  for (; step + kDepth <= end; step += kDepth) {
+    Part x[kDepth];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    sums[wave][0][j][lane] = acc[0][j];
-    sums[wave][1][j][lane] = acc[1][j];
+    for (int i = 0; i < kDepth; ++i) load(x[i], step + i);
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) add(x[i]);
   }
+  for (; step < end; ++step) {
+    Part x;
+    load(x, step);
+    add(x);
+  }
+  if (wave == 3 && bytes % kStepBytes) {
+    Part x;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) x.v[i][h] = load_part(from[i] + steps * kStepBytes, 16 * h, bytes % kStepBytes - g * 32);
+    add(x);
+  }
+  sums[wave][0][lane] = acc[0];
+  sums[wave][1][lane] = acc[1];
   __syncthreads();
-  for (int j = wave; j < MT; j += 4) {
+  if (wave == 0 && r < p.rows) {
     f32x4 t[2];
 #pragma unroll
     for (int w = 0; w < 2; ++w)
-      t[w] = (sums[0][w][j][lane] + sums[1][w][j][lane]) + (sums[2][w][j][lane] + sums[3][w][j][lane]);
-    const int64_t m = 16 * j + r;
-    if (m >= p.rows) continue;
+      t[w] = (sums[0][w][lane] + sums[1][w][lane]) + (sums[2][w][lane] + sums[3][w][lane]);
+    const int64_t m = r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int n = n0 + 4 * g + i;
@@ -206,6 +229,7 @@ __global__ __launch_bounds__(256) void gated_forward_few_kernel(const Forward p)
       }
     }
   }
+#endif
 }
 
 // ------------------------------------------------------------- backward
@@ -220,6 +244,8 @@ struct Backward {
   uint16_t* dwg;
   uint16_t* dwu;
   char* both;           // [rows][2*width]: dg, then du
+  float* parts;         // dx before the last sum, [splits][rows][d]
+  int splits;           // parts that dx's k is cut into
   int64_t rows, width;  // width: f rounded up to 64
   int64_t ldx, ldw;     // bytes
   int64_t lddh, ldg, lddx, lddw;
@@ -270,116 +296,169 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(const Backward p) {
   }
 }
 
+// The wave's sums to rows m0 + mrow.. and columns n0.. of a [rows, cols] matrix;
+// of several teams each stores its share.
+template <class T, class G, class Out>
+__device__ __forceinline__ void store_tile(Out* out, int64_t ld, int64_t rows, int cols, int64_t m0, int mrow, int n0,
+                                           int team, bool vec, const f32x4 (&acc)[G::MT][G::NT]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < G::MT; ++j) {
+    const int64_t m = m0 + row_of(mrow, j);
+    if (m >= rows) continue;
+#pragma unroll
+    for (int q = 0; q < G::NT / 2; ++q) {
+      if (G::kTeams > 1 && (j * (G::NT / 2) + q) % G::kTeams != team) continue;
+      const int n = n0 + 32 * q + 8 * (lane >> 4);
+      float v[8];
+      take8(acc, q, j, v);
+      if constexpr (std::is_same<T, float>::value) store8(out + m * ld + n, v, cols - n, vec);
+      else store8<T>(out + m * ld + n, v, cols - n, vec);
+    }
+  }
+}
+
 // dx = [dg du] [Wg; Wu]: k runs along the rows of the weights.
-template <class T, int B>
-__global__ __launch_bounds__(256, B == 256 ? 1 : 2) void gated_dx_kernel(const Backward p) {
+template <class T, class G>
+__global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dx_kernel(const Backward p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int T16 = B / 32, HALF = B / 2;
-  __shared__ __align__(16) char lds[2][2 * B * kStepBytes];
+  constexpr int S = G::kSize, KG = G::kTeams;
+  __shared__ __align__(16) typename G::Lds lds;
   int tm, tn;
   tile_of_group(p.tiles_m, p.tiles_n, p.band, tm, tn);
-  const int wave = wave_id(), lane = threadIdx.x & 63;
-  const int mrow = (wave >> 1) * HALF, ncol = (wave & 1) * HALF;
-  const int64_t m0 = int64_t{tm} * B;
-  const int n0 = tn * B;
+  const int team = wave_id() / G::NW, wave = wave_id() % G::NW;
+  const int mrow = wave / G::WN * (S / G::WM), ncol = wave % G::WN * (S / G::WN);
+  const int64_t m0 = int64_t{tm} * S;
+  const int n0 = tn * S;
   const int64_t lda = 4 * p.width;
-  Loader<kRows, B, 4> la;
-  Loader<kCols, B, 4> lb;
-  la.init(p.both + m0 * lda, lda, std::min<int64_t>(B, p.rows - m0) * lda, 0, wave);
+  Loader<kRows, S, G::NW> la;
+  Loader<kCols, S, G::NW> lb;
+  la.init(p.both + m0 * lda, lda, std::min<int64_t>(S, p.rows - m0) * lda, 0, wave);
   lb.init(p.wg + 2 * n0, p.ldw, (p.f - 1) * p.ldw + ((2 * int64_t{p.d} + 15) & ~int64_t{15}) - 2 * n0, p.d - n0, wave);
-  const int half = static_cast<int>(p.width / 64);
-  auto at_step = [&](int step) {
-    la.at_step(step, (2 * half - step) * kStepBytes);
+  // blockIdx.y: the part of k
+  const int half = static_cast<int>(p.width / 64), per = (2 * half + p.splits - 1) / p.splits;
+  const int begin = blockIdx.y * per, end = std::min(2 * half, begin + per), steps = (end - begin + KG - 1) / KG;
+  auto at_step = [&](int s) {
+    const int step = begin + s * KG + team;
+    la.at_step(step, (end - step) * kStepBytes);
     lb.base = (step < half ? p.wg : p.wu) + 2 * n0;
-    lb.at_step(step < half ? step : step - half, 0);
+    lb.at_step(step >= end ? 2 * half : step < half ? step : step - half, 0);
   };
   auto issue = [&](int j, uint32_t to, int i) {
     if (i == 0) la.issue(to, j);
-    else lb.issue(to + B * kStepBytes, j);
+    else lb.issue(to + S * kStepBytes, j);
   };
-  f32x4 acc[T16][T16];
-  multiply<T, kRows, kCols, B, B, 2, 2>(lds, 0, 2 * half, mrow, ncol, ncol + HALF / 2, at_step, issue, [](char*) {}, acc);
-#pragma unroll
-  for (int j = 0; j < T16; ++j) {
-    const int64_t m = m0 + row_of(mrow, j);
-    if (m >= p.rows) continue;
-#pragma unroll
-    for (int q = 0; q < T16 / 2; ++q) {
-      const int n = n0 + ncol + 32 * q + 8 * (lane >> 4);
-      float v[8];
-      take8(acc, q, j, v);
-      store8<T>(p.dx + m * p.lddx + n, v, p.d - n, p.vec);
-    }
-  }
+  f32x4 acc[G::MT][G::NT];
+  multiply<T, G, kRows, kCols>(lds[team], steps, mrow, ncol, ncol + S / G::WN / 2, at_step, issue, [](char*) {}, acc);
+  add_teams<KG, G::NW>(lds, team, wave, acc);
+  if (p.splits == 1)
+    store_tile<T, G>(p.dx, p.lddx, p.rows, p.d, m0, mrow, n0 + ncol, team, p.vec, acc);
+  else
+    store_tile<float, G>(p.parts + blockIdx.y * p.rows * p.d, p.d, p.rows, p.d, m0, mrow, n0 + ncol, team, p.d % 4 == 0, acc);
 #endif
 }
 
+// dx from its parts, added in their order.
+template <class T>
+__global__ __launch_bounds__(256) void gated_dx_sum_kernel(const Backward p) {
+  const int64_t total = p.rows * p.d;
+  for (int64_t at = int64_t{blockIdx.x} * 256 + threadIdx.x; at < total; at += int64_t{gridDim.x} * 256) {
+    float v = p.parts[at];
+    for (int i = 1; i < p.splits; ++i) v += p.parts[i * total + at];
+    p.dx[at / p.d * p.lddx + at % p.d] = static_cast<uint16_t>(bits_of(T{}, v));
+  }
+}
+
 // dWg = dg^T x and dWu = du^T x: k is the rows (tokens) of both operands.
-template <class T, int B>
-__global__ __launch_bounds__(256, B == 256 ? 1 : 2) void gated_dw_kernel(const Backward p) {
+template <class T, class G>
+__global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dw_kernel(const Backward p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int T16 = B / 32, HALF = B / 2;
-  __shared__ __align__(16) char lds[2][2 * B * kStepBytes];
+  constexpr int S = G::kSize, KG = G::kTeams;
+  __shared__ __align__(16) typename G::Lds lds;
   int tm, tn;
   tile_of_group(p.tiles_m, p.tiles_n, p.band, tm, tn);
-  const int wave = wave_id(), lane = threadIdx.x & 63;
-  const int mrow = (wave >> 1) * HALF, ncol = (wave & 1) * HALF;
+  const int team = wave_id() / G::NW, wave = wave_id() % G::NW;
+  const int mrow = wave / G::WN * (S / G::WM), ncol = wave % G::WN * (S / G::WN);
   const int one = p.tiles_m / 2;
   const bool second = tm >= one;
-  const int f0 = (second ? tm - one : tm) * B, n0 = tn * B;
+  const int f0 = (second ? tm - one : tm) * S, n0 = tn * S;
   const int64_t lda = 4 * p.width;
-  Loader<kCols, B, 4> la, lb;
+  Loader<kCols, S, G::NW> la, lb;
   const int64_t off = 2 * (f0 + (second ? p.width : 0));
   la.init(p.both + off, lda, p.rows * lda - off, static_cast<int>(p.width) - f0, wave);
   lb.init(p.x + 2 * n0, p.ldx, (p.rows - 1) * p.ldx + ((2 * int64_t{p.d} + 15) & ~int64_t{15}) - 2 * n0, p.d - n0, wave);
-  auto at_step = [&](int step) {
-    la.at_step(step, 0);
-    lb.at_step(step, 0);
+  auto at_step = [&](int s) {
+    la.at_step(s * KG + team, 0);
+    lb.at_step(s * KG + team, 0);
   };
   auto issue = [&](int j, uint32_t to, int i) {
     if (i == 0) la.issue(to, j);
-    else lb.issue(to + B * kStepBytes, j);
+    else lb.issue(to + S * kStepBytes, j);
   };
-  const int steps = static_cast<int>((p.rows + 63) / 64);
-  f32x4 acc[T16][T16];
-  multiply<T, kCols, kCols, B, B, 2, 2>(lds, 0, steps, mrow, ncol, ncol + HALF / 2, at_step, issue, [](char*) {}, acc);
-  uint16_t* out = second ? p.dwu : p.dwg;
-#pragma unroll
-  for (int j = 0; j < T16; ++j) {
-    const int64_t m = f0 + row_of(mrow, j);
-    if (m >= p.f) continue;
-#pragma unroll
-    for (int q = 0; q < T16 / 2; ++q) {
-      const int n = n0 + ncol + 32 * q + 8 * (lane >> 4);
-      float v[8];
-      take8(acc, q, j, v);
-      store8<T>(out + m * p.lddw + n, v, p.d - n, p.vec);
-    }
-  }
+  const int steps = static_cast<int>((p.rows + 64 * KG - 1) / (64 * KG));
+  f32x4 acc[G::MT][G::NT];
+  multiply<T, G, kCols, kCols>(lds[team], steps, mrow, ncol, ncol + S / G::WN / 2, at_step, issue, [](char*) {}, acc);
+  add_teams<KG, G::NW>(lds, team, wave, acc);
+  store_tile<T, G>(second ? p.dwu : p.dwg, p.lddw, p.f, p.d, f0, mrow, n0 + ncol, team, p.vec, acc);
 #endif
 }
 
 bool wide(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * 2 % 16 == 0; }
 
+// Microseconds that `tiles` tiles of `steps` steps take, `at_once` of them side by
+// side on the chip: a full round runs steps * step + fixed, a last round of at
+// most 256 tiles (one to a CU) steps * step_few + fixed_few.
+double estimate(int64_t tiles, int64_t steps, int at_once, double step, double fixed, double step_few, double fixed_few) {
+  const int64_t rest = tiles % at_once;
+  const double full = static_cast<double>(steps) * step + fixed;
+  const double last = rest == 0 ? 0.0 : rest <= 256 ? static_cast<double>(steps) * step_few + fixed_few : full;
+  return static_cast<double>(tiles / at_once) * full + last;
+}
+
+// Calls f with the tiling that covers `products` results of m x n, k long, in the
+// least time by the estimate, and with the tiles that gives.  The constants fit
+// these measurements (us; dx is m x n = rows x d, k = 2f):
+//                                     256     128   128x2 teams  64x2   64x4
+//   dx   500 x 1024, k  8192          178      84        65       46     36
+//   dx  2048 x 1024, k  8192          177      85        67       54     74
+//   dx  2048 x 2560, k 20480          445     269       342      385    523
+//   dx  4096 x 4096, k  8192          206     254       281      389    558
+//   dw  8192 x 1024, k   500           22      15        20       28     43
+//   h    500 x 8192, k  1024           30      15        14       19     28
+//   h   8192 x 32768, k 4096         1784    2094      3089     3940   5942
+template <class F>
+void with_tiling(int64_t m, int64_t n, int64_t k, int64_t products, F&& f) {
+  auto tiles = [&](int64_t size) { return products * ((m + size - 1) / size) * ((n + size - 1) / size); };
+  const int64_t steps = (k + 63) / 64;
+  const double cost[5] = {
+      estimate(tiles(256), steps, 256, 1.65, 12, 1.45, 12),
+      estimate(tiles(128), steps, 512, 0.97, 7, 0.66, 5),
+      estimate(tiles(128), steps, 256, 0.52, 6, 0.50, 6),
+      estimate(tiles(64), steps, 512, 0.40, 3.5, 0.34, 3),
+      estimate(tiles(64), steps, 256, 0.285, 3.5, 0.28, 3.5),
+  };
+  switch (std::min_element(cost, cost + 5) - cost) {
+    case 0: return f(Tiling<256, 1>{});
+    case 1: return f(Tiling<128, 1>{});
+    case 2: return f(Tiling<128, 2>{});
+    case 3: return f(Tiling<64, 2>{});
+    default: return f(Tiling<64, 4>{});
+  }
+}
+
 template <class T>
 hipError_t forward(Forward p, hipStream_t stream) {
-  if (p.rows <= 64) {
-    const unsigned grid = static_cast<unsigned>((p.f + 15) / 16);
-    if (p.rows <= 16) gated_forward_few_kernel<T, 1><<<grid, 256, 0, stream>>>(p);
-    else if (p.rows <= 32) gated_forward_few_kernel<T, 2><<<grid, 256, 0, stream>>>(p);
-    else gated_forward_few_kernel<T, 4><<<grid, 256, 0, stream>>>(p);
+  if (p.rows <= 16) {
+    gated_forward_few_kernel<T><<<(p.f + 15) / 16, 256, 0, stream>>>(p);
     return hipGetLastError();
   }
-  auto tiles = [&](int bm, int bn) {
-    p.tiles_m = (p.rows + bm - 1) / bm;
-    p.tiles_n = (p.f + bn / 2 - 1) / (bn / 2);
+  with_tiling(p.rows, 2 * int64_t{p.f}, p.d, 1, [&](auto g) {
+    typedef decltype(g) G;
+    p.tiles_m = (p.rows + G::kSize - 1) / G::kSize;
+    p.tiles_n = (p.f + G::kSize / 2 - 1) / (G::kSize / 2);
     p.band = std::min(8, p.tiles_m);
-    return static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-  };
-  if (const int64_t t = tiles(256, 256); t >= 200)
-    gated_forward_kernel<T, 256><<<static_cast<unsigned>(t), 256, 0, stream>>>(p);
-  else
-    gated_forward_kernel<T, 128><<<static_cast<unsigned>(tiles(128, 128)), 256, 0, stream>>>(p);
+    gated_forward_kernel<T, G><<<p.tiles_m * p.tiles_n, G::kThreads, 0, stream>>>(p);
+  });
   return hipGetLastError();
 }
 
@@ -390,35 +469,33 @@ hipError_t backward(Backward p, hipStream_t stream) {
     gated_slopes_kernel<T><<<static_cast<unsigned>(std::min<int64_t>((chunks + 255) / 256, 1 << 20)), 256, 0, stream>>>(p);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  auto tiles = [&](int64_t m, int64_t n, int b) {
-    p.tiles_m = static_cast<int>((m + b - 1) / b);
-    p.tiles_n = static_cast<int>((n + b - 1) / b);
-    return static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  auto cover = [&](int64_t m, int64_t n, int size) {
+    p.tiles_m = static_cast<int>((m + size - 1) / size);
+    p.tiles_n = static_cast<int>((n + size - 1) / size);
   };
   if (p.dx && p.rows > 0) {
     p.vec = wide(p.dx, p.lddx);
-    if (tiles(p.rows, p.d, 256) >= 200) {
+    with_tiling(p.rows, p.d, 2 * p.width / p.splits, p.splits, [&](auto g) {
+      typedef decltype(g) G;
+      cover(p.rows, p.d, G::kSize);
       p.band = std::min(8, p.tiles_m);
-      gated_dx_kernel<T, 256><<<p.tiles_m * p.tiles_n, 256, 0, stream>>>(p);
-    } else {
-      tiles(p.rows, p.d, 128);
-      p.band = std::min(8, p.tiles_m);
-      gated_dx_kernel<T, 128><<<p.tiles_m * p.tiles_n, 256, 0, stream>>>(p);
-    }
+      gated_dx_kernel<T, G><<<dim3(p.tiles_m * p.tiles_n, p.splits), G::kThreads, 0, stream>>>(p);
+    });
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (p.splits > 1) {
+      gated_dx_sum_kernel<T><<<static_cast<unsigned>((p.rows * p.d + 255) / 256), 256, 0, stream>>>(p);
+      if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
   }
   if (p.dwg) {
     p.vec = wide(p.dwg, p.lddw) && wide(p.dwu, p.lddw);
-    if (2 * tiles(p.f, p.d, 256) >= 200) {
+    with_tiling(p.f, p.d, p.rows, 2, [&](auto g) {
+      typedef decltype(g) G;
+      cover(p.f, p.d, G::kSize);
       p.tiles_m *= 2;
       p.band = std::min(8, p.tiles_m);
-      gated_dw_kernel<T, 256><<<p.tiles_m * p.tiles_n, 256, 0, stream>>>(p);
-    } else {
-      tiles(p.f, p.d, 128);
-      p.tiles_m *= 2;
-      p.band = std::min(8, p.tiles_m);
-      gated_dw_kernel<T, 128><<<p.tiles_m * p.tiles_n, 256, 0, stream>>>(p);
-    }
+      gated_dw_kernel<T, G><<<p.tiles_m * p.tiles_n, G::kThreads, 0, stream>>>(p);
+    });
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -459,6 +536,8 @@ hipError_t launch_gated_ffn_backward(const opt8_gated_ffn_grad& a, hipStream_t s
   p.dwg = static_cast<uint16_t*>(a.dw_gate);
   p.dwu = static_cast<uint16_t*>(a.dw_up);
   p.both = static_cast<char*>(a.workspace);
+  p.parts = reinterpret_cast<float*>(p.both + gated_bytes(a.rows, a.f));
+  p.splits = gated_dx_splits(a.rows, a.d, a.f);
   p.rows = a.rows;
   p.width = gated_width(a.f);
   p.ldx = 2 * a.ldx;

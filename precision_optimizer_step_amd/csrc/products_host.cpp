@@ -238,5 +238,5 @@ extern "C" int opt8_gated_ffn_backward(const opt8_gated_ffn_grad* grad, void* hi
 
 extern "C" int64_t opt8_gated_ffn_workspace(int64_t rows, int64_t d, int64_t f) {
   if (rows < 0 || d < 0 || f < 0 || rows > opt8::kMaxCount || d > opt8::kMaxWidth || f > opt8::kMaxWidth) return 0;
-  return opt8::gated_bytes(rows, f);
+  return opt8::gated_workspace(rows, d, f);
 }

@@ -268,11 +268,25 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
-// The steps of one tile of a 16-bit product.  at_step(step) turns both operands'
-// loaders to a step, issue(j, to, i) queues the wave's j-th load of A (i = 0,
-// first in a copy) or B, last(t) finishes the last step's copy before it is read.
-// The wave's rows of A start at `mrow`, its columns at `ncol0` (first half of
-// them) and `ncol1`.  acc[j][q]: matrix tile j of the wave's rows, q of its columns.
+// A tiling of a 16-bit product: S x S tiles, in each team of waves WM of them
+// along the rows and WN along the columns, KG teams that take the steps in turn
+// (each with copies of its own) and add their sums at the end.
+template <int S, int KG>
+struct Tiling {
+  static constexpr int kSize = S, kTeams = KG;
+  static constexpr int WM = 2, WN = S == 64 ? 1 : 2, NW = WM * WN;   // 32 x 64, 64 x 64 or 128 x 128 to a wave
+  static constexpr int MT = S / WM / 16, NT = S / WN / 16;
+  static constexpr int kThreads = 64 * NW * KG, kMinWaves = S == 256 ? 1 : 2;
+  static constexpr int kCopy = 2 * S * kStepBytes;
+  typedef char Lds[KG][2][kCopy];
+};
+
+// The steps of one tile.  at_step(s) turns both operands' loaders to the team's
+// step s, issue(j, to, i) queues the wave's j-th load of A (i = 0, first in a
+// copy) or B, last(t) finishes the last step's copy before it is read (called by
+// every team at the same step).  The wave's rows of A start at `mrow`, its
+// columns at `ncol0` (first half of them) and `ncol1`.  acc[j][q]: matrix tile j
+// of the wave's rows, q of its columns.
 //
 // Half a step (32 k) is in registers while the other half is on its way from
 // LDS, so between two barriers a wave has a whole step of matrix instructions
@@ -281,14 +295,12 @@ __device__ __forceinline__ void wait_and_meet() {
 // at_step() is called for two steps past the last one too; their loads are out
 // of range and bring zeros without touching memory, which is cheaper than
 // leaving them out (a second copy of the loop's body).
-template <class T, Layout LA, Layout LB, int BM, int BN, int WM, int WN, class Step, class Issue, class Last>
-__device__ __forceinline__ void multiply(char (*lds)[(BM + BN) * kStepBytes], int first, int steps, int mrow, int ncol0,
-                                         int ncol1, Step&& at_step, Issue&& issue, Last&& last,
-                                         f32x4 (&acc)[BM / WM / 16][BN / WN / 16]) {
-  constexpr int MT = BM / WM / 16, NT = BN / WN / 16, kLoads = BM / 8 / (WM * WN);
-  static_assert(MT == NT && kLoads == MT && BM == BN, "one load of each operand goes with each row of matrix tiles");
-  Reader<LA, BM, MT / 2> ra;
-  Reader<LB, BN, NT / 4> rb[2];
+template <class T, class G, Layout LA, Layout LB, class Step, class Issue, class Last>
+__device__ __forceinline__ void multiply(char (*lds)[G::kCopy], int steps, int mrow, int ncol0, int ncol1, Step&& at_step,
+                                         Issue&& issue, Last&& last, f32x4 (&acc)[G::MT][G::NT]) {
+  constexpr int S = G::kSize, MT = G::MT, NT = G::NT, kLoads = S / 8 / G::NW;
+  Reader<LA, S, MT / 2> ra;
+  Reader<LB, S, NT / 4> rb[2];
   ra.init(mrow);
   rb[0].init(ncol0);
   rb[1].init(ncol1);
@@ -297,67 +309,76 @@ __device__ __forceinline__ void multiply(char (*lds)[(BM + BN) * kStepBytes], in
 #pragma unroll
     for (int q = 0; q < NT; ++q) acc[j][q] = f32x4{0, 0, 0, 0};
   if (steps <= 0) return;
-  constexpr uint32_t kCopy = (BM + BN) * kStepBytes;
   const uint32_t copies = lds_address(lds);
   settle(acc);
-  at_step(first);
+  at_step(0);
 #pragma unroll
-  for (int j = 0; j < 2 * kLoads; ++j) issue(j / 2, copies, j % 2);
-  at_step(first + 1);
+  for (int l = 0; l < 2 * kLoads; ++l) issue(l / 2, copies, l % 2);
+  at_step(1);
 #pragma unroll
-  for (int j = 0; j < 2 * kLoads; ++j) issue(j / 2, copies + kCopy, j % 2);
+  for (int l = 0; l < 2 * kLoads; ++l) issue(l / 2, copies + G::kCopy, l % 2);
   wait_and_meet<2 * kLoads>();
   if (steps == 1) last(lds[0]);
   i32x4 a[2][MT], b[2][NT];
+  // Read r of a half step's MT + NT: what its first row of matrix tiles needs comes first.
+  auto read = [&](const char* from, int h, int r) {
+    if (r == 0) a[h][0] = ra.read(from, 0, h);
+    else if (r <= NT) b[h][r - 1] = rb[(r - 1) / (NT / 2)].read(from + S * kStepBytes, (r - 1) % (NT / 2), h);
+    else a[h][r - NT] = ra.read(from, r - NT, h);
+  };
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    a[0][j] = ra.read(lds[0], j, 0);
-    b[0][j] = rb[j / (NT / 2)].read(lds[0] + BM * kStepBytes, j % (NT / 2), 0);
-  }
-  // One row of matrix tiles; between its pairs of matrix instructions (32 cycles
-  // each) fit what prepare(0..NT/2-1) asks for: a single wave issues an
-  // instruction every 4 cycles, so a longer gap would leave the matrix core idle.
-  auto row = [&](int j, int h, auto&& prepare) {
+  for (int r = 0; r < MT + NT; ++r) read(lds[0], 0, r);
+  // The matrix instructions of half a step in pairs, with what is to be read and
+  // loaded spread between them: a pair runs 32 cycles and a single wave issues an
+  // instruction every 4, so a longer gap would leave the matrix core idle.
+  constexpr int kPairs = MT * NT / 2, kReads = MT + NT, kAll = kReads + 2 * kLoads;
+  auto half = [&](int h, int count, auto&& prepare) {
 #pragma unroll
-    for (int q = 0; q < NT; q += 2) {
-      prepare(q / 2);
+    for (int i = 0; i < kPairs; ++i) {
+#pragma unroll
+      for (int o = 0; o < kAll; ++o)
+        if (o < count && (count <= kPairs ? o == i : o * kPairs / count == i)) prepare(o);
+      const int j = i / (NT / 2), q = i % (NT / 2) * 2;
       mfma_pair<T>(acc[j][q], acc[j][q + 1], b[h][q], b[h][q + 1], a[h][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // Read r of a half step's MT + NT: what its first row of matrix tiles needs comes first.
-  auto read = [&](const char* from, int h, int r) {
-    if (r == 0) a[h][0] = ra.read(from, 0, h);
-    else if (r <= NT) b[h][r - 1] = rb[(r - 1) / (NT / 2)].read(from + BM * kStepBytes, (r - 1) % (NT / 2), h);
-    else a[h][r - NT] = ra.read(from, r - NT, h);
-  };
-  constexpr int kPairs = NT / 2, kReads = MT + NT, kAll = kReads + 2 * kLoads, kEach = kAll / (MT * kPairs);
-  static_assert(kAll == kEach * MT * kPairs && kReads <= MT * kPairs, "what is read and loaded fits between the pairs");
   for (int s = 0; s < steps; ++s) {
     const char* t = lds[s & 1];
     const char* next = lds[(s + 1) & 1];
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-      row(j, 0, [&](int i) {
-        if (j * kPairs + i < kReads) read(t, 1, j * kPairs + i);
-      });
+    half(0, kReads, [&](int o) { read(t, 1, o); });
     wait_and_meet();
     if (s + 2 == steps) last(lds[(s + 1) & 1]);
-    at_step(first + s + 2);
+    at_step(s + 2);
     // the loads first: they have the longest way
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-      row(j, 1, [&](int i) {
-#pragma unroll
-        for (int n = 0; n < kEach; ++n) {
-          const int o = (j * kPairs + i) * kEach + n;
-          if (o < 2 * kLoads) issue(o / 2, copies + (s & 1) * kCopy, o % 2);
-          else read(next, 0, o - 2 * kLoads);
-        }
-      });
+    half(1, kAll, [&](int o) {
+      if (o < 2 * kLoads) issue(o / 2, copies + (s & 1) * G::kCopy, o % 2);
+      else read(next, 0, o - 2 * kLoads);
+    });
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load outlives the workgroup's LDS
   settle(acc);
+}
+
+// Adds the teams' sums, in the order of the teams; every team gets the result.
+template <int KG, int NW, int MT, int NT, class L>
+__device__ __forceinline__ void add_teams(L& lds, int team, int wave, f32x4 (&acc)[MT][NT]) {
+  if constexpr (KG > 1) {
+    static_assert(sizeof(L) >= KG * NW * MT * NT * 64 * sizeof(f32x4), "the copies hold the sums");
+    f32x4* sums = reinterpret_cast<f32x4*>(lds);
+    const int lane = threadIdx.x & 63;
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < MT * NT; ++t) sums[((team * NW + wave) * MT * NT + t) * 64 + lane] = acc[t / NT][t % NT];
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < MT * NT; ++t) {
+      f32x4 v = sums[(wave * MT * NT + t) * 64 + lane];
+#pragma unroll
+      for (int g = 1; g < KG; ++g) v += sums[((g * NW + wave) * MT * NT + t) * 64 + lane];
+      acc[t / NT][t % NT] = v;
+    }
+  }
 }
 
 // m (within the workgroup's tile) of matrix tile j, for this lane.
@@ -399,6 +420,17 @@ __device__ __forceinline__ void store8(uint16_t* p, const float* v, int64_t left
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < left) p[i] = static_cast<uint16_t>(bits_of(T{}, v[i]));
+  }
+}
+
+__device__ __forceinline__ void store8(float* p, const float* v, int64_t left, bool vec) {
+  if (vec && left >= 8) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = v[i];
   }
 }
 

@@ -199,6 +199,26 @@ def test_backward_largest_tiles(rows, d, f):
     check_backward(rows, d, f, seed=6)
 
 
+@pytest.mark.parametrize("rows,f", [(17, 4000), (130, 4100), (500, 4104), (1500, 4104), (2050, 4104)])
+def test_forward_every_tile_size(rows, f):
+    """64 x 64 tiles with four teams of waves and with two, 128 x 128 with two and with one, and
+    256 x 256, at depths that give the teams different numbers of steps, and none to some."""
+    for d in (60, 129, 320):
+        check_forward(rows, d, f, seed=d)
+
+
+@pytest.mark.parametrize("rows,d,f", [(1, 128, 4096), (64, 130, 4096), (70, 1000, 2080), (500, 1024, 1100), (17, 9, 3000)])
+def test_backward_with_a_long_sum_for_dx(rows, d, f):
+    """dx from several parts of its contraction (2f), some shorter than others."""
+    assert ops.opt8_gated_ffn_workspace(rows, d, f) > rows * 4 * (-(-f // 64) * 64)
+    check_backward(rows, d, f, seed=rows)
+
+
+@pytest.mark.parametrize("rows,d,f", [(600, 2100, 700), (1100, 2100, 500), (1, 700, 300), (3000, 130, 260)])
+def test_backward_every_tile_size(rows, d, f):
+    check_backward(rows, d, f, seed=8)
+
+
 def test_backward_of_no_rows_clears_the_weights_gradients():
     e = torch.empty(0, 64, dtype=BF, device="cuda")
     w = torch.randn(96, 64, generator=gen(0)).to(BF).cuda()
