@@ -27,6 +27,7 @@
 
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 
 #include <hip/hip_runtime.h>
 
@@ -46,6 +47,16 @@ typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
 struct Bf16 {};
 struct Fp16 {};
+
+// f(0), f(1), ... f(N - 1), each with its number as a constant.
+template <class F, int... I>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+  each_of(std::make_integer_sequence<int, N>{}, f);
+}
 
 enum Layout : int { kRows = 0, kCols = 1 };
 
@@ -145,8 +156,8 @@ struct Loader {
   // register: the compiler keeps nothing in it and no other instruction here reads it.)
   __device__ __forceinline__ void issue(uint32_t to, int j) const {
 #if defined(__HIP_DEVICE_COMPILE__)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(to + lds0 + j * 1024), "v"(voff[j]), "s"(range), "s"(soff));
+    asm volatile("s_add_i32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(to + lds0), "v"(voff[j]), "s"(range), "s"(soff), "s"(1024 * j) : "scc");
 #endif
   }
 };
@@ -228,19 +239,13 @@ template <>
 __device__ __forceinline__ f32x4 mfma16<Fp16>(i32x4 b, i32x4 a, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
 }
-// x += b0 a and y += b1 a.  In asm, so that the sums stay where they are: with the
-// builtins the compiler moves them between the two halves of the register file
-// inside the loop (210 moves beside 128 matrix instructions).  The nop covers a
-// vector instruction that wrote an operand right before; the sums are read only
-// after settle().
+// x += b a.  The empty asm keeps the sum in the accumulation half of the register
+// file: left alone, the compiler moves sums between the halves inside the loop
+// (210 moves beside 128 matrix instructions).
 template <class T>
-__device__ __forceinline__ void mfma_pair(f32x4& x, f32x4& y, const i32x4& b0, const i32x4& b1, const i32x4& a) {
-  if constexpr (std::is_same<T, Bf16>::value)
-    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %2, %4, %0\n\tv_mfma_f32_16x16x32_bf16 %1, %3, %4, %1"
-                 : "+a"(x), "+a"(y) : "v"(b0), "v"(b1), "v"(a));
-  else
-    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %2, %4, %0\n\tv_mfma_f32_16x16x32_f16 %1, %3, %4, %1"
-                 : "+a"(x), "+a"(y) : "v"(b0), "v"(b1), "v"(a));
+__device__ __forceinline__ void mfma_add(f32x4& x, const i32x4& b, const i32x4& a) {
+  x = mfma16<T>(b, a, x);
+  asm volatile("" : "+a"(x));
 }
 // Orders the sums behind a wait longer than any of these instructions runs (4
 // passes of 4 cycles): after writing zeros to them, and before reading them.
@@ -328,30 +333,31 @@ __device__ __forceinline__ void multiply(char (*lds)[G::kCopy], int steps, int m
   };
 #pragma unroll
   for (int r = 0; r < MT + NT; ++r) read(lds[0], 0, r);
-  // The matrix instructions of half a step in pairs, with what is to be read and
-  // loaded spread between them: a pair runs 32 cycles and a single wave issues an
-  // instruction every 4, so a longer gap would leave the matrix core idle.
-  constexpr int kPairs = MT * NT / 2, kReads = MT + NT, kAll = kReads + 2 * kLoads;
-  auto half = [&](int h, int count, auto&& prepare) {
+  // The matrix instructions of half a step, with what is to be read and loaded
+  // spread between them: each runs 16 cycles and a single wave issues an
+  // instruction every 4, so at most three fit behind one.
+  constexpr int kSlots = MT * NT, kReads = MT + NT, kAll = kReads + 2 * kLoads;
+  auto half = [&](int h, auto count, auto&& prepare) {
+    // operation o goes behind matrix instruction o * kSlots / kSpread
+    constexpr int kCount = decltype(count)::value, kSpread = kSlots < kAll ? kCount : kAll;
+    each<kSlots>([&](auto slot) {
+      constexpr int i = decltype(slot)::value, j = i / NT, q = i % NT;
+      mfma_add<T>(acc[j][q], b[h][q], a[h][j]);
+      constexpr int begin = (i * kSpread + kSlots - 1) / kSlots, end = ((i + 1) * kSpread + kSlots - 1) / kSlots;
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-#pragma unroll
-      for (int o = 0; o < kAll; ++o)
-        if (o < count && (count <= kPairs ? o == i : o * kPairs / count == i)) prepare(o);
-      const int j = i / (NT / 2), q = i % (NT / 2) * 2;
-      mfma_pair<T>(acc[j][q], acc[j][q + 1], b[h][q], b[h][q + 1], a[h][j]);
+      for (int o = begin; o < (end < kCount ? end : kCount); ++o) prepare(o);
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
   };
   for (int s = 0; s < steps; ++s) {
     const char* t = lds[s & 1];
     const char* next = lds[(s + 1) & 1];
-    half(0, kReads, [&](int o) { read(t, 1, o); });
+    half(0, std::integral_constant<int, kReads>{}, [&](int o) { read(t, 1, o); });
     wait_and_meet();
     if (s + 2 == steps) last(lds[(s + 1) & 1]);
     at_step(s + 2);
     // the loads first: they have the longest way
-    half(1, kAll, [&](int o) {
+    half(1, std::integral_constant<int, kAll>{}, [&](int o) {
       if (o < 2 * kLoads) issue(o / 2, copies + (s & 1) * G::kCopy, o % 2);
       else read(next, 0, o - 2 * kLoads);
     });
