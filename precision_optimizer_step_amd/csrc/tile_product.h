@@ -334,33 +334,66 @@ __device__ __forceinline__ void multiply(char (*lds)[G::kCopy], int steps, int m
 #pragma unroll
   for (int r = 0; r < MT + NT; ++r) read(lds[0], 0, r);
   // The matrix instructions of half a step, with what is to be read and loaded
-  // spread between them: each runs 16 cycles and a single wave issues an
-  // instruction every 4, so at most three fit behind one.
-  constexpr int kSlots = MT * NT, kReads = MT + NT, kAll = kReads + 2 * kLoads;
-  auto half = [&](int h, auto count, auto&& prepare) {
-    // operation o goes behind matrix instruction o * kSlots / kSpread
-    constexpr int kCount = decltype(count)::value, kSpread = kSlots < kAll ? kCount : kAll;
-    each<kSlots>([&](auto slot) {
-      constexpr int i = decltype(slot)::value, j = i / NT, q = i % NT;
+  // spread between them by prepare(place): each runs 16 cycles and a single wave
+  // issues an instruction every 4, so at most three fit behind one.
+  constexpr int kPlaces = MT * NT, kReads = MT + NT, kAll = kReads + 2 * kLoads;
+  auto half = [&](int h, auto&& prepare) {
+    each<kPlaces>([&](auto place) {
+      constexpr int i = decltype(place)::value, j = i / NT, q = i % NT;
       mfma_add<T>(acc[j][q], b[h][q], a[h][j]);
-      constexpr int begin = (i * kSpread + kSlots - 1) / kSlots, end = ((i + 1) * kSpread + kSlots - 1) / kSlots;
-#pragma unroll
-      for (int o = begin; o < (end < kCount ? end : kCount); ++o) prepare(o);
+      prepare(place);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
   for (int s = 0; s < steps; ++s) {
     const char* t = lds[s & 1];
     const char* next = lds[(s + 1) & 1];
-    half(0, std::integral_constant<int, kReads>{}, [&](int o) { read(t, 1, o); });
-    wait_and_meet();
-    if (s + 2 == steps) last(lds[(s + 1) & 1]);
-    at_step(s + 2);
-    // the loads first: they have the longest way
-    half(1, std::integral_constant<int, kAll>{}, [&](int o) {
-      if (o < 2 * kLoads) issue(o / 2, copies + (s & 1) * G::kCopy, o % 2);
-      else read(next, 0, o - 2 * kLoads);
-    });
+    const uint32_t to = copies + (s & 1) * G::kCopy;
+    if constexpr (kPlaces >= 64) {
+      // 256 x 256.  Four waves' loads at one for every 2 matrix instructions are
+      // twice what the CU's cache path takes (64 bytes a cycle), and the wave that
+      // waits to issue one cannot issue matrix instructions either.  So the waves
+      // meet in the first half too, once the copy has been read, and the loads that
+      // fill it again go behind every sixth instruction from there on.
+      constexpr int kMeet = 36, kEvery = 6, kEarly = (kPlaces - kMeet + kEvery - 1) / kEvery;
+      half(0, [&](auto place) {
+        constexpr int i = decltype(place)::value;
+        if constexpr (i % 2 == 0 && i / 2 < kReads) read(t, 1, i / 2);
+        if constexpr (i == kMeet) {
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          at_step(s + 2);
+        }
+        if constexpr (i >= kMeet && (i - kMeet) % kEvery == 0) issue((i - kMeet) / kEvery / 2, to, (i - kMeet) / kEvery % 2);
+      });
+      wait_and_meet<kEarly>();
+      if (s + 2 == steps) last(lds[(s + 1) & 1]);
+      half(1, [&](auto place) {
+        constexpr int i = decltype(place)::value, l = kEarly + i / kEvery;
+        if constexpr (i % kEvery == 0 && l < 2 * kLoads) issue(l / 2, to, l % 2);
+        if constexpr (i % 4 == 2) read(next, 0, i / 4);
+      });
+      static_assert(kPlaces / 4 == kReads && (2 * kLoads - kEarly - 1) * kEvery < kPlaces, "all is read and loaded");
+    } else {
+      // smaller tiles: other waves of the SIMD fill the gaps
+      auto in_place = [&](auto place, auto count, auto&& f) {
+        constexpr int i = decltype(place)::value, n = decltype(count)::value;
+        constexpr int begin = (i * n + kPlaces - 1) / kPlaces, end = ((i + 1) * n + kPlaces - 1) / kPlaces;
+#pragma unroll
+        for (int o = begin; o < end; ++o) f(o);
+      };
+      half(0, [&](auto place) {
+        in_place(place, std::integral_constant<int, kReads>{}, [&](int o) { read(t, 1, o); });
+      });
+      wait_and_meet();
+      if (s + 2 == steps) last(lds[(s + 1) & 1]);
+      at_step(s + 2);
+      half(1, [&](auto place) {
+        in_place(place, std::integral_constant<int, kAll>{}, [&](int o) {
+          if (o < 2 * kLoads) issue(o / 2, to, o % 2);     // the longest way first
+          else read(next, 0, o - 2 * kLoads);
+        });
+      });
+    }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load outlives the workgroup's LDS
   settle(acc);
