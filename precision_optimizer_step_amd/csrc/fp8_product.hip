@@ -85,6 +85,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Pro
   };
   // the wave's load l of the step: its parts of A, of B, its scales
   constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW, kAll = kA + kB + 1;
+  // With one workgroup to a CU (256 x 256), the loads of a step are more than the
+  // CU's cache path takes (64 bytes a cycle) in the two rows behind the barrier,
+  // and waves that wait to issue one stand still: some go to the next two rows.
+  constexpr int kLater = MT == 8 ? 4 : 0, kNow = kAll - kLater;
   const uint32_t copies = lds_address(lds);
   auto issue = [&](uint32_t to, int l) {
     if (l < kA) la.issue(to, l);
@@ -162,6 +166,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Pro
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         constexpr bool two = MT == 2;     // both rows are read at the end of the step before
+        if (kLater && j < 2 && (4 * j + q) % 2 == 1)      // what was left of the next step's loads
+          issue(copies + ((step + 1) & 1) * kCopy, kNow + (4 * j + q) / 2);
         if (!two && j < MT - 2) {
           if (q == 0) read_a(step, j + 1);
           if (q == 2 && j == MT - 3) read_a(step, MT - 1);
@@ -169,8 +175,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Pro
           // the last two rows: 8 places for the loads, B and the next first row
           const int at = (j - (MT - 2)) * 4 + q;
 #pragma unroll
-          for (int l = 0; l < kAll; ++l)
-            if (l * 6 / kAll == at) issue(copies + (step & 1) * kCopy, l);
+          for (int l = 0; l < kNow; ++l)
+            if (l * 6 / kNow == at) issue(copies + (step & 1) * kCopy, l);
           if (at >= 2 && at < 6) read_b(step + 1, 1 - S, at - 2);
           if (!two && at == 6) read_a(step + 1, 0);
         }
@@ -195,8 +201,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Pro
     for (int l = 0; l < kAll; ++l) issue(copies, l);
     at_step(1);
 #pragma unroll
-    for (int l = 0; l < kAll; ++l) issue(copies + kCopy, l);
-    wait_and_meet<kAll>();
+    for (int l = 0; l < kNow; ++l) issue(copies + kCopy, l);
+    wait_and_meet<kNow>();
     clear(0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) read_b(0, 0, q);

@@ -25,10 +25,31 @@ struct Quant {
 template <class X> struct Raw { typedef uint16_t type; };
 template <> struct Raw<float> { typedef float type; };
 
-// 8 consecutive values; `left` of them exist, the others are zero.
+// 8 consecutive values as they lie in memory (16-bit ones stay packed until they
+// are used: 32 registers for a thread's 64 values instead of 64); `left` of them
+// exist, the others are zero.
 template <class X>
-__device__ __forceinline__ void load8(const typename Raw<X>::type* p, int64_t left, bool vec, float* v) {
-  if constexpr (std::is_same<X, float>::value) {
+struct Eight {
+  i16x8 v;
+  __device__ __forceinline__ void zero() { v = i16x8{0, 0, 0, 0, 0, 0, 0, 0}; }
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t left, bool vec) {
+    if (vec && left >= 8) {
+      v = *reinterpret_cast<const i16x8*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < left ? static_cast<short>(p[i]) : 0;
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const { return value_of<X>(static_cast<uint16_t>(v[i])); }
+};
+template <>
+struct Eight<float> {
+  float v[8];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  }
+  __device__ __forceinline__ void load(const float* p, int64_t left, bool vec) {
     if (vec && left >= 8) {
       const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
 #pragma unroll
@@ -37,16 +58,21 @@ __device__ __forceinline__ void load8(const typename Raw<X>::type* p, int64_t le
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
     }
-  } else {
-    if (vec && left >= 8) {
-      const i16x8 a = *reinterpret_cast<const i16x8*>(p);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = value_of<X>(static_cast<uint16_t>(a[i]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < left ? value_of<X>(p[i]) : 0.0f;
-    }
   }
+  __device__ __forceinline__ float operator[](int i) const { return v[i]; }
+};
+
+// The largest of the 16 lanes of a row, in every one of them: rotations by 1, 2,
+// 4 and 8 lanes.
+template <int CONTROL>
+__device__ __forceinline__ float rotated(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CONTROL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float largest_of_16(float x) {
+  x = __builtin_fmaxf(x, rotated<0x121>(x));
+  x = __builtin_fmaxf(x, rotated<0x122>(x));
+  x = __builtin_fmaxf(x, rotated<0x124>(x));
+  return __builtin_fmaxf(x, rotated<0x128>(x));
 }
 
 // The largest magnitude so far; NaN does not count (fmaxf returns the other).
@@ -84,16 +110,12 @@ __global__ __launch_bounds__(256) void quantize_kernel(const Quant p) {
   const int cblk = blockIdx.x % p.cb, rblk = blockIdx.x / p.cb;
   const int64_t r0 = int64_t{rblk} * 128 + rg * 8, c0 = int64_t{cblk} * 128 + lane16 * 8;
   const auto* x = static_cast<const typename Raw<X>::type*>(p.x);
-  float v[8][8];
+  Eight<X> v[8];
   const int64_t cleft = p.cols - c0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (r0 + i < p.rows && cleft > 0) {
-      load8<X>(x + (r0 + i) * p.ldx + c0, cleft, p.vec, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    }
+    if (r0 + i < p.rows && cleft > 0) v[i].load(x + (r0 + i) * p.ldx + c0, cleft, p.vec);
+    else v[i].zero();
   }
 
   float inv[8], invt[8];
@@ -103,8 +125,9 @@ __global__ __launch_bounds__(256) void quantize_kernel(const Quant p) {
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = larger(top, v[i][j]);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    top = largest_of_16(top);
+    top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+    top = __builtin_fmaxf(top, __shfl_xor(top, 32));
     if ((t & 63) == 0) wave_top[t >> 6] = top;
     __syncthreads();
     top = __builtin_fmaxf(__builtin_fmaxf(wave_top[0], wave_top[1]), __builtin_fmaxf(wave_top[2], wave_top[3]));
@@ -122,9 +145,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const Quant p) {
         float top = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = larger(top, v[i][j]);
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-        const float s = scale_of<F>(top);
+        const float s = scale_of<F>(largest_of_16(top));
         inv[i] = 1.0f / s;
         if (lane16 == i && r0 + i < p.rows) p.scale[int64_t{cblk} * p.rows + r0 + i] = s;
       }

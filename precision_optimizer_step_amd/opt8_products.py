@@ -121,18 +121,14 @@ def _scales(what, t, blocks, across):
 
 def _placed(*tensors):
     """All on one GPU, and that one current (a call queues on the current device)."""
-    first = None
+    first = tensors[0][1].get_device()
     for what, t in tensors:
-        if t is None:
-            continue
-        if first is None:
-            first = t.device
-        elif t.device != first:
-            raise ValueError(f"{what}: on {t.device}, but {tensors[0][0]} is on {first}")
-    if first.type != "cuda":
-        raise ValueError(f"{tensors[0][0]}: on {first}; the operators run on a GPU")
-    if first.index != torch.cuda.current_device():
-        raise ValueError(f"{tensors[0][0]}: on {first}, but the current device is cuda:{torch.cuda.current_device()}")
+        if t is not None and t.get_device() != first:
+            raise ValueError(f"{what}: on {t.device}, but {tensors[0][0]} is on {tensors[0][1].device}")
+    if first < 0:
+        raise ValueError(f"{tensors[0][0]}: on {tensors[0][1].device}; the operators run on a GPU")
+    if first != torch.cuda.current_device():
+        raise ValueError(f"{tensors[0][0]}: on cuda:{first}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _ceil(n):
@@ -269,8 +265,15 @@ def opt8_gated_ffn_workspace(rows: int, d: int, f: int) -> int:
 
 
 # ----------------------------------------------------------------------------- calls
+def _current_stream():
+    # torch.cuda.current_stream() builds an object for it (3 us, as long as a whole small call)
+    if torch.cuda.is_initialized():
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _stream_handle(None)
+
+
 def _call(name, desc, stream, check):
-    rc = _functions()[name](desc, _stream_handle(stream) or None)
+    rc = _functions()[name](desc, (_current_stream() if stream is None else _stream_handle(stream)) or None)
     return _check(rc) if check else rc
 
 
