@@ -33,7 +33,7 @@ __device__ __forceinline__ void activate(float g, float& value, float& slope) {
     // Phi(-x) = phi(x) R(x) for x >= 0.  Mills' ratio R is smooth in t = 1/(1 +
     // 0.285 x): R = t * (a polynomial of degree 8 in t), minimax by reweighted least
     // squares on [0, inf), 1.6e-7 relative, 5e-7 in fp32.  About 14 instructions
-    // where erfcf takes 60 (an epilogue of 255 us at 8192 x 16384 against 30).
+    // where erfcf takes 60 (8192 x 16384 results: 59 us more than silu, against 255).
     const float x = __builtin_fabsf(g);
     const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.285f, x, 1.0f));
     float r = 0.0615863354f;
@@ -129,24 +129,40 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_forward_kerne
   multiply<T, G, kRows, kRows>(lds[team], steps, mrow, ncol, HALF + ncol, at_step, issue, last, acc);
   add_teams<KG, G::NW>(lds, team, wave, acc);
 
+  constexpr int NG = G::NT / 4;       // 32-column groups of h in the wave's part
+  constexpr bool kRowsOut = KG == 1 && NG > 1;
+  const bool rows_out = kRowsOut && p.vec && f0 + HALF <= p.f;
+  char* scratch = lds[0][0] + wave * kRowScratch<NG>;
+  if constexpr (kRowsOut) __syncthreads();       // other waves may still read the copies
   with_act(p.act, [&](auto act) {
 #pragma unroll
     for (int j = 0; j < G::MT; ++j) {
       const int64_t m = m0 + row_of(mrow, j);
+      float g[NG][8], u[NG][8], h[NG][8];
+#pragma unroll
+      for (int q = 0; q < NG; ++q) {
+        take8(acc, q, j, g[q]);
+        take8(acc, q + NG, j, u[q]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[q][i] = activate<decltype(act)::value>(g[q][i]) * u[q][i];
+      }
+      if (rows_out) {
+        store_rows<T>(scratch, p.h + f0 + ncol, p.ldh, p.rows, m0, mrow, j, h);
+        if (p.gate) {
+          store_rows<T>(scratch, p.gate + f0 + ncol, p.ldg, p.rows, m0, mrow, j, g);
+          store_rows<T>(scratch, p.up + f0 + ncol, p.ldg, p.rows, m0, mrow, j, u);
+        }
+        continue;
+      }
       if (m >= p.rows) continue;
 #pragma unroll
-      for (int q = 0; q < G::NT / 4; ++q) {
-        if (KG > 1 && (j * (G::NT / 4) + q) % KG != team) continue;    // each team its share
+      for (int q = 0; q < NG; ++q) {
+        if (KG > 1 && (j * NG + q) % KG != team) continue;    // each team its share
         const int n = f0 + ncol + 32 * q + 8 * (lane >> 4);
-        float g[8], u[8], h[8];
-        take8(acc, q, j, g);
-        take8(acc, q + G::NT / 4, j, u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = activate<decltype(act)::value>(g[i]) * u[i];
-        store8<T>(p.h + m * p.ldh + n, h, p.f - n, p.vec);
+        store8<T>(p.h + m * p.ldh + n, h[q], p.f - n, p.vec);
         if (p.gate) {
-          store8<T>(p.gate + m * p.ldg + n, g, p.f - n, p.vec);
-          store8<T>(p.up + m * p.ldg + n, u, p.f - n, p.vec);
+          store8<T>(p.gate + m * p.ldg + n, g[q], p.f - n, p.vec);
+          store8<T>(p.up + m * p.ldg + n, u[q], p.f - n, p.vec);
         }
       }
     }
@@ -314,18 +330,32 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(const Backward p) {
 }
 
 // The wave's sums to rows m0 + mrow.. and columns n0.. of a [rows, cols] matrix;
-// of several teams each stores its share.
+// of several teams each stores its share.  scratch: the wave's part of the copies.
 template <class T, class G, class Out>
-__device__ __forceinline__ void store_tile(Out* out, int64_t ld, int64_t rows, int cols, int64_t m0, int mrow, int n0,
-                                           int team, bool vec, const f32x4 (&acc)[G::MT][G::NT]) {
+__device__ __forceinline__ void store_tile(char* scratch, Out* out, int64_t ld, int64_t rows, int cols, int64_t m0, int mrow,
+                                           int n0, int team, bool vec, const f32x4 (&acc)[G::MT][G::NT]) {
+  constexpr int NG = G::NT / 2;
   const int lane = threadIdx.x & 63;
+  if constexpr (G::kTeams == 1 && !std::is_same<T, float>::value) {
+    __syncthreads();       // other waves may still read the copies
+    if (vec && n0 + 32 * NG <= cols) {
+#pragma unroll
+      for (int j = 0; j < G::MT; ++j) {
+        float v[NG][8];
+#pragma unroll
+        for (int q = 0; q < NG; ++q) take8(acc, q, j, v[q]);
+        store_rows<T>(scratch, out + n0, ld, rows, m0, mrow, j, v);
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < G::MT; ++j) {
     const int64_t m = m0 + row_of(mrow, j);
     if (m >= rows) continue;
 #pragma unroll
-    for (int q = 0; q < G::NT / 2; ++q) {
-      if (G::kTeams > 1 && (j * (G::NT / 2) + q) % G::kTeams != team) continue;
+    for (int q = 0; q < NG; ++q) {
+      if (G::kTeams > 1 && (j * NG + q) % G::kTeams != team) continue;
       const int n = n0 + 32 * q + 8 * (lane >> 4);
       float v[8];
       take8(acc, q, j, v);
@@ -369,9 +399,9 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dx_kernel(con
   multiply<T, G, kRows, kCols>(lds[team], steps, mrow, ncol, ncol + S / G::WN / 2, at_step, issue, [](char*) {}, acc);
   add_teams<KG, G::NW>(lds, team, wave, acc);
   if (p.splits == 1)
-    store_tile<T, G>(p.dx, p.lddx, p.rows, p.d, m0, mrow, n0 + ncol, team, p.vec, acc);
+    store_tile<T, G>(lds[0][0] + wave * kRowScratch<G::NT / 2>, p.dx, p.lddx, p.rows, p.d, m0, mrow, n0 + ncol, team, p.vec, acc);
   else
-    store_tile<float, G>(p.parts + blockIdx.y * p.rows * p.d, p.d, p.rows, p.d, m0, mrow, n0 + ncol, team, p.d % 4 == 0, acc);
+    store_tile<float, G>(nullptr, p.parts + blockIdx.y * p.rows * p.d, p.d, p.rows, p.d, m0, mrow, n0 + ncol, team, p.d % 4 == 0, acc);
 #endif
 }
 
@@ -416,7 +446,7 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dw_kernel(con
   f32x4 acc[G::MT][G::NT];
   multiply<T, G, kCols, kCols>(lds[team], steps, mrow, ncol, ncol + S / G::WN / 2, at_step, issue, [](char*) {}, acc);
   add_teams<KG, G::NW>(lds, team, wave, acc);
-  store_tile<T, G>(second ? p.dwu : p.dwg, p.lddw, p.f, p.d, f0, mrow, n0 + ncol, team, p.vec, acc);
+  store_tile<T, G>(lds[0][0] + wave * kRowScratch<G::NT / 2>, second ? p.dwu : p.dwg, p.lddw, p.f, p.d, f0, mrow, n0 + ncol, team, p.vec, acc);
 #endif
 }
 
