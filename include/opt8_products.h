@@ -15,14 +15,14 @@
  *
  * Matrices are row-major with `ld` elements from one row to the next.
  * Operands that feed the matrix cores (every input, and the 8-bit outputs)
- * start on a 16-byte boundary, have ld*size a multiple of 16, and own rows*ld
- * elements (in a view, the bytes between the end of a row and the next are
- * read and ignored; they are never written).  Other outputs need their
+ * start on a 16-byte boundary, have ld*size a multiple of 16, and own the last
+ * 16 bytes of their last row whole (rows are read in pieces of 16 bytes; what
+ * lies behind a row's end is ignored, and never written).  Other outputs need their
  * element's own alignment only and are faster on 16 bytes.  No count of rows
  * or columns exceeds 2^22 (d and f: 2^20), no matrix 2^37 elements, and no
- * ld*size of a matrix that feeds the matrix cores 2^23 bytes.  The span of an
- * output (first to last element) may not overlap that of another buffer of the
- * call.
+ * ld*size of a matrix that feeds the matrix cores 2^23 bytes.  An output may
+ * not overlap another buffer of the call; halves of one wider matrix (the same
+ * ld, columns side by side) are apart, other spans that meet are refused.
  *
  * Status codes of these calls: OPT8_E_NULL (a required pointer), OPT8_E_SIZE
  * (counts, ld, workspace), OPT8_E_MODE (an unknown type, block or act, or a

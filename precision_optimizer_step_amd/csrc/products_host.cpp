@@ -47,6 +47,20 @@ struct Matrix {
 // Bytes from the first to past the last element.
 int64_t span(const Matrix& x) { return ((x.rows - 1) * x.ld + x.cols) * x.size; }
 
+// Whether two matrices share a byte.  Spans that meet are still apart where both
+// have the same distance between rows and their columns lie side by side in it
+// (two halves of one wider matrix).
+bool overlap(const Matrix& x, const Matrix& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  if (a + span(x) <= b || b + span(y) <= a) return false;
+  const int64_t pitch = x.ld * x.size;
+  if (pitch != y.ld * y.size) return true;
+  const int64_t wx = x.cols * x.size, wy = y.cols * y.size;
+  int64_t at = static_cast<int64_t>(b - a) % pitch;     // where y's row starts in x's
+  if (at < 0) at += pitch;
+  return at < wx || at + wy > pitch;
+}
+
 int check_count(const char* name, int64_t v, int64_t low, int64_t high) {
   if (v < low || v > high)
     return refuse(OPT8_E_SIZE, "%s must be %lld to %lld (got %lld)", name, static_cast<long long>(low),
@@ -74,11 +88,9 @@ int check_matrices(const Matrix* list, int n) {
   }
   for (int i = 0; i < n; ++i) {
     if (!list[i].p || !list[i].output || list[i].rows <= 0 || list[i].cols <= 0) continue;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(list[i].p), hi = lo + span(list[i]);
     for (int j = 0; j < n; ++j) {
       if (j == i || !list[j].p || list[j].rows <= 0 || list[j].cols <= 0) continue;
-      const uintptr_t a = reinterpret_cast<uintptr_t>(list[j].p), b = a + span(list[j]);
-      if (a < hi && lo < b) return refuse(OPT8_E_ALIAS, "%s overlaps %s", list[i].name, list[j].name);
+      if (overlap(list[i], list[j])) return refuse(OPT8_E_ALIAS, "%s overlaps %s", list[i].name, list[j].name);
     }
   }
   return OPT8_OK;

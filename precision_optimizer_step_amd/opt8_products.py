@@ -89,8 +89,8 @@ def _functions():
 # ----------------------------------------------------------------------------- checks
 def _matrix(what, t, dtypes, rows, cols, owned=False):
     """The row distance of a [rows, cols] torch matrix with dense rows.  owned: the
-    elements between the end of a row and the next, behind the last row too, must
-    belong to the tensor's storage (the library reads them in 16-byte pieces)."""
+    last row's last 16 bytes must belong to the tensor's storage whole (the library
+    reads rows in pieces of 16)."""
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: dtype {t.dtype} not allowed here (expected one of "
                          f"{', '.join(str(d) for d in dtypes)})")
@@ -105,8 +105,10 @@ def _matrix(what, t, dtypes, rows, cols, owned=False):
         # a single row's distance is arbitrary: the smallest that keeps 16-byte rows
         each = max(1, 16 // t.element_size())
         step = -(-cols // each) * each if owned else cols
-    if owned and rows and cols and t.storage_offset() + rows * step > t.untyped_storage().nbytes() // t.element_size():
-        raise ValueError(f"{what}: its storage ends before the last row's {step} elements")
+    if owned and rows and cols:
+        each = 16 // t.element_size()
+        if t.storage_offset() + (rows - 1) * step + -(-cols // each) * each > t.untyped_storage().nbytes() // t.element_size():
+            raise ValueError(f"{what}: its storage ends inside the last 16 bytes of the last row")
     return step
 
 

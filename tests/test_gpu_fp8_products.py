@@ -343,3 +343,55 @@ def test_library_refusals_reach_the_caller():
     with pytest.raises(opt8.Opt8Error) as e:
         ops.opt8_fp8_matmul(p)
     assert e.value.status == opt8.OPT8_E_ALIAS
+
+
+def test_offsets_past_32_bits():
+    """x, codes and results of over 2^31 elements: the last rows are as those of a small call."""
+    rows, cols, n = 70003, 32784, 32784
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    qt_store, qt = code_room(cols, rows, E4)
+    q = torch.empty(rows, cols, dtype=torch.uint8, device="cuda").view(E4)
+    s, st = torch.empty(ref.ceil128(cols), rows, device="cuda"), torch.empty(ref.ceil128(rows), cols, device="cuda")
+    ops.opt8_fp8_quantize(ops.make_fp8_quant(x, q, s, qt, st))
+    torch.cuda.synchronize()
+    tail = x[-83:]                       # the last block of rows (70003 = 546 * 128 + 115) ends here
+    want, ws = ref.quantize(tail, E4, False)
+    assert torch.equal(q[-83:].view(torch.uint8).cpu(), want) and torch.equal(s[:, -83:].cpu(), ws)
+    want, ws = ref.quantize(x[-115:].t()[-40:], E4, False)
+    assert torch.equal(qt[-40:, -115:].view(torch.uint8).cpu(), want) and torch.equal(st[-1:, -40:].cpu(), ws)
+    del x, qt, qt_store
+    k = 144
+    a = q.as_strided((rows, k), (cols, 1), cols - k)       # the last columns: rows of q, far apart
+    b = q.as_strided((n, k), (cols, 1), 16)
+    sa, sb = torch.ones(2, rows, device="cuda"), torch.ones(2, ref.ceil128(n), device="cuda")
+    a_own = torch.empty(rows + 1, cols, dtype=torch.uint8, device="cuda").view(E4)   # owns what lies behind the last row
+    a_own.view(torch.uint8)[:rows].copy_(q.view(torch.uint8))
+    a = a_own.as_strided((rows, k), (cols, 1), cols - k)
+    b = a_own.as_strided((n, k), (cols, 1), 16)
+    del q
+    c = torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda")
+    ops.opt8_fp8_matmul(ops.make_fp8_product(a, sa, b, sb, c))
+    torch.cuda.synchronize()
+    for r in (slice(0, 40), slice(rows - 60, rows)):
+        want, bound = ref.product(a[r], sa[:, r], b[-50:], torch.ones(2, 1, device="cuda"), True)
+        assert ref.worst(c[r, -50:], want, ref.rounded(want, bound, torch.bfloat16)) <= 1.0
+
+
+def test_two_streams_at_once():
+    """Different calls on two streams without order between them: each as alone."""
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sets = [operands(300, 500, 1024, E4, True, s) for s in (31, 32)]
+    alone = []
+    for a, sa, b, sb in sets:
+        c = torch.empty(300, 500, dtype=torch.bfloat16, device="cuda")
+        ops.opt8_fp8_matmul(ops.make_fp8_product(a, sa, b, sb, c))
+        alone.append(c)
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(c) for c in alone]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for side, (a, sa, b, sb), c in zip(sides, sets, outs):
+            ops.opt8_fp8_matmul(ops.make_fp8_product(a, sa, b, sb, c), stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(alone, outs))

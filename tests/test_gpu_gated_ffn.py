@@ -374,3 +374,53 @@ def test_training_step_through_every_operator():
 
 def wd_of(bits, rows, cols):
     return torch.from_numpy(bits.view(np.int16).copy()).view(torch.bfloat16).double().view(rows, cols)
+
+
+def test_projections_as_halves_of_one_matrix():
+    """gate and up side by side in one [rows, 2f] matrix, forward and back; both weights in one [2f, d]."""
+    rows, d, f = 150, 64, 104
+    x, _, _ = inputs(rows, d, f, BF, 60)
+    w = (torch.randn(2 * f, d, generator=gen(61)) * d ** -0.5).to(BF).cuda()
+    both = torch.zeros(rows, 2 * f, dtype=BF, device="cuda")
+    h, g, u = (torch.empty(rows, f, dtype=BF, device="cuda") for _ in range(3))
+    ops.opt8_gated_ffn_forward(ops.make_gated_ffn(x, w[:f], w[f:], h, both[:, :f], both[:, f:]))
+    h2 = torch.empty_like(h)
+    ops.opt8_gated_ffn_forward(ops.make_gated_ffn(x, w[:f].clone(), w[f:].clone(), h2, g, u))
+    torch.cuda.synchronize()
+    assert torch.equal(h, h2) and torch.equal(both[:, :f], g) and torch.equal(both[:, f:], u)
+    work = torch.empty(ops.opt8_gated_ffn_workspace(rows, d, f), dtype=torch.uint8, device="cuda")
+    res = []
+    for gate, up in ((both[:, :f], both[:, f:]), (g, u)):
+        dx, dw = torch.empty(rows, d, dtype=BF, device="cuda"), torch.empty(2 * f, d, dtype=BF, device="cuda")
+        ops.opt8_gated_ffn_backward(ops.make_gated_ffn_grad(h, x, w[:f], w[f:], gate, up, dx, dw[:f], dw[f:], work))
+        torch.cuda.synchronize()
+        res.append((dx, dw))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
+def test_offsets_past_32_bits():
+    """Projections, their gradients and the workspace of over 2^31 elements."""
+    rows, d, f = 140003, 64, 16400
+    x, wg, wu = inputs(rows, d, f, BF, 70)
+    x, wg, wu = x.contiguous(), wg.contiguous(), wu.contiguous()
+    h, g, u = (torch.empty(rows, f, dtype=BF, device="cuda") for _ in range(3))
+    ops.opt8_gated_ffn_forward(ops.make_gated_ffn(x, wg, wu, h, g, u))
+    torch.cuda.synchronize()
+    for r in (slice(0, 30), slice(rows - 30, rows)):
+        want, err = forward_reference(x[r], wg, wu, "silu")
+        for got, w, e in zip((h, g, u), want, err):
+            assert ref.worst(got[r], w, ref.rounded(w, e, BF)) <= 1.0
+    # gradients: dh nonzero in the first and last rows only, so that 64-bit sums stay short
+    h.zero_()
+    for r in (slice(0, 30), slice(rows - 30, rows)):
+        h[r] = torch.randn(30, f, generator=gen(71)).to(BF)
+    dx, dg, du = torch.empty(rows, d, dtype=BF, device="cuda"), torch.empty_like(wg), torch.empty_like(wu)
+    work = torch.empty(ops.opt8_gated_ffn_workspace(rows, d, f), dtype=torch.uint8, device="cuda")
+    ops.opt8_gated_ffn_backward(ops.make_gated_ffn_grad(h, x, wg, wu, g, u, dx, dg, du, work))
+    torch.cuda.synchronize()
+    keep = torch.cat([torch.arange(30), torch.arange(rows - 30, rows)]).cuda()
+    want, err = grad_reference(h[keep], x[keep], wg, wu, g[keep], u[keep], "silu", BF)
+    assert ref.worst(dx[keep], want[0], ref.rounded(want[0], err[0], BF)) <= 1.0
+    assert bool((dx[30:rows - 30] == 0).all())
+    for got, w, e in ((dg, want[1], err[1]), (du, want[2], err[2])):
+        assert ref.worst(got, w, ref.rounded(w, e, BF)) <= 1.0

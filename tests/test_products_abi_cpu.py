@@ -172,6 +172,20 @@ def test_gated_backward_refusals(L, over, status, fragment):
     expect(grad(**over), status, fragment)
 
 
+def test_halves_of_one_matrix_do_not_overlap(L):
+    """gate and up as the column halves of one [rows, 2f] matrix, and the cases next to it."""
+    g = A + 4 * STEP
+    assert ffn(gate=g, up=g + 2 * 96, ldg=192) in REACHED
+    assert ffn(gate=g + 2 * 96, up=g, ldg=192) in REACHED
+    expect(ffn(gate=g, up=g + 2 * 96 - 2, ldg=192), ALIAS, "overlaps")
+    expect(ffn(gate=g, up=g + 2 * 97, ldg=192), ALIAS, "overlaps")
+    expect(ffn(gate=g, up=g + 2 * 96, ldg=191), ALIAS, "overlaps")
+    expect(ffn(gate=g, h=g + 2 * 96, ldg=192, ldh=384), ALIAS, "overlaps")
+    assert ffn(rows=1, gate=g, up=g + 2 * 96, ldg=96) in REACHED
+    assert quant(rows=100, q=A + STEP, ldq=416, qt=A + 3 * STEP, x=A + STEP + 208, x_type=ops.OPT8_TYPE_BF16, cols=100,
+                 ldx=208) in REACHED      # x beside q in rows of 416 bytes
+
+
 def test_one_sided_backward_needs_only_its_inputs(L):
     assert grad(dx=None, w_gate=None, w_up=None) in REACHED
     assert grad(dw_gate=None, dw_up=None, x=None) in REACHED
