@@ -217,19 +217,20 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Pro
 
   // each team finishes its share of the 32-column groups
   add_teams<KG, NW, MT, 4>(lds_all, team, wave, acc);
+  __syncthreads();       // other waves may still read what the results are staged in
+  constexpr int NG = KG == 1 ? 2 : 1;
+  char* scratch = lds_all[0][0] + (team * NW + wave) * kRowScratch<NG>;
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int m = m0 + wm * (BM / WM) + (j >> 1) * 32 + 4 * (j & 1) + mlane;
-    if (m >= p.m) continue;
+  for (int j = 0; j < MT; ++j)
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < 2; q += NG) {
       if (KG > 1 && (2 * j + q) % KG != team) continue;
-      const int n = n0 + wn * 64 + q * 32 + 8 * (lane >> 4);
-      float v[8];
-      take8(acc, q, j, v);
-      store8<C>(p.c + m * p.ldc + n, v, p.n - n, p.vec);
+      const int n = n0 + wn * 64 + q * 32;
+      float v[NG][8];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) take8(acc, q + i, j, v[i]);
+      if (n < p.n) store_rows<C, NG>(scratch, p.c + n, p.ldc, p.m, p.n - n, p.vec, m0, wm * (BM / WM), j, v);
     }
-  }
 #endif
 }
 

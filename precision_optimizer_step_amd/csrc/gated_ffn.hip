@@ -96,7 +96,7 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_forward_kerne
   __shared__ __align__(16) typename G::Lds lds;
   int tm, tn;
   tile_of_group(p.tiles_m, p.tiles_n, p.band, tm, tn);
-  const int lane = threadIdx.x & 63, team = wave_id() / G::NW, wave = wave_id() % G::NW;
+  const int team = wave_id() / G::NW, wave = wave_id() % G::NW;
   const int mrow = wave / G::WN * (S / G::WM), ncol = wave % G::WN * (HALF / G::WN);
   const int m0 = tm * S, f0 = tn * HALF;
   const int kbytes = 2 * p.d;
@@ -130,42 +130,31 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_forward_kerne
   add_teams<KG, G::NW>(lds, team, wave, acc);
 
   constexpr int NG = G::NT / 4;       // 32-column groups of h in the wave's part
-  constexpr bool kRowsOut = KG == 1 && NG > 1;
-  const bool rows_out = kRowsOut && p.vec && f0 + HALF <= p.f;
-  char* scratch = lds[0][0] + wave * kRowScratch<NG>;
-  if constexpr (kRowsOut) __syncthreads();       // other waves may still read the copies
+  constexpr int NS = KG == 1 ? NG : 1;    // of them stored together
+  char* scratch = lds[0][0] + (team * G::NW + wave) * kRowScratch<NS>;
+  __syncthreads();       // other waves may still read what the results are staged in
   with_act(p.act, [&](auto act) {
 #pragma unroll
-    for (int j = 0; j < G::MT; ++j) {
-      const int64_t m = m0 + row_of(mrow, j);
-      float g[NG][8], u[NG][8], h[NG][8];
+    for (int j = 0; j < G::MT; ++j)
 #pragma unroll
-      for (int q = 0; q < NG; ++q) {
-        take8(acc, q, j, g[q]);
-        take8(acc, q + NG, j, u[q]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[q][i] = activate<decltype(act)::value>(g[q][i]) * u[q][i];
-      }
-      if (rows_out) {
-        store_rows<T>(scratch, p.h + f0 + ncol, p.ldh, p.rows, m0, mrow, j, h);
-        if (p.gate) {
-          store_rows<T>(scratch, p.gate + f0 + ncol, p.ldg, p.rows, m0, mrow, j, g);
-          store_rows<T>(scratch, p.up + f0 + ncol, p.ldg, p.rows, m0, mrow, j, u);
-        }
-        continue;
-      }
-      if (m >= p.rows) continue;
-#pragma unroll
-      for (int q = 0; q < NG; ++q) {
+      for (int q = 0; q < NG; q += NS) {
         if (KG > 1 && (j * NG + q) % KG != team) continue;    // each team its share
-        const int n = f0 + ncol + 32 * q + 8 * (lane >> 4);
-        store8<T>(p.h + m * p.ldh + n, h[q], p.f - n, p.vec);
+        const int n = f0 + ncol + 32 * q;
+        if (n >= p.f) continue;
+        float g[NS][8], u[NS][8], h[NS][8];
+#pragma unroll
+        for (int t = 0; t < NS; ++t) {
+          take8(acc, q + t, j, g[t]);
+          take8(acc, q + t + NG, j, u[t]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[t][i] = activate<decltype(act)::value>(g[t][i]) * u[t][i];
+        }
+        store_rows<T, NS>(scratch, p.h + n, p.ldh, p.rows, p.f - n, p.vec, m0, mrow, j, h);
         if (p.gate) {
-          store8<T>(p.gate + m * p.ldg + n, g[q], p.f - n, p.vec);
-          store8<T>(p.up + m * p.ldg + n, u[q], p.f - n, p.vec);
+          store_rows<T, NS>(scratch, p.gate + n, p.ldg, p.rows, p.f - n, p.vec, m0, mrow, j, g);
+          store_rows<T, NS>(scratch, p.up + n, p.ldg, p.rows, p.f - n, p.vec, m0, mrow, j, u);
         }
       }
-    }
   });
 #endif
 }
@@ -330,39 +319,36 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(const Backward p) {
 }
 
 // The wave's sums to rows m0 + mrow.. and columns n0.. of a [rows, cols] matrix;
-// of several teams each stores its share.  scratch: the wave's part of the copies.
+// of several teams each stores its share.
 template <class T, class G, class Out>
-__device__ __forceinline__ void store_tile(char* scratch, Out* out, int64_t ld, int64_t rows, int cols, int64_t m0, int mrow,
-                                           int n0, int team, bool vec, const f32x4 (&acc)[G::MT][G::NT]) {
-  constexpr int NG = G::NT / 2;
-  const int lane = threadIdx.x & 63;
-  if constexpr (G::kTeams == 1 && !std::is_same<T, float>::value) {
-    __syncthreads();       // other waves may still read the copies
-    if (vec && n0 + 32 * NG <= cols) {
+__device__ __forceinline__ void store_tile(char* copies, Out* out, int64_t ld, int64_t rows, int cols, int64_t m0, int mrow,
+                                           int n0, int team, int wave, bool vec, const f32x4 (&acc)[G::MT][G::NT]) {
+  constexpr int NG = G::NT / 2, KG = G::kTeams, NS = KG == 1 ? NG : 1;
+  char* scratch = copies + (team * G::NW + wave) * kRowScratch<NS>;
+  __syncthreads();       // other waves may still read what the results are staged in
 #pragma unroll
-      for (int j = 0; j < G::MT; ++j) {
-        float v[NG][8];
+  for (int j = 0; j < G::MT; ++j)
 #pragma unroll
-        for (int q = 0; q < NG; ++q) take8(acc, q, j, v[q]);
-        store_rows<T>(scratch, out + n0, ld, rows, m0, mrow, j, v);
+    for (int q = 0; q < NG; q += NS) {
+      if (KG > 1 && (j * NG + q) % KG != team) continue;
+      const int n = n0 + 32 * q;
+      if (n >= cols) continue;
+      if constexpr (std::is_same<T, float>::value) {
+        const int64_t m = m0 + row_of(mrow, j);
+        const int at = n + 8 * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+        for (int t = 0; t < NS; ++t) {
+          float v[8];
+          take8(acc, q + t, j, v);
+          if (m < rows) store8(out + m * ld + at + 32 * t, v, cols - at - 32 * t, vec);
+        }
+      } else {
+        float v[NS][8];
+#pragma unroll
+        for (int t = 0; t < NS; ++t) take8(acc, q + t, j, v[t]);
+        store_rows<T, NS>(scratch, out + n, ld, rows, cols - n, vec, m0, mrow, j, v);
       }
-      return;
     }
-  }
-#pragma unroll
-  for (int j = 0; j < G::MT; ++j) {
-    const int64_t m = m0 + row_of(mrow, j);
-    if (m >= rows) continue;
-#pragma unroll
-    for (int q = 0; q < NG; ++q) {
-      if (G::kTeams > 1 && (j * NG + q) % G::kTeams != team) continue;
-      const int n = n0 + 32 * q + 8 * (lane >> 4);
-      float v[8];
-      take8(acc, q, j, v);
-      if constexpr (std::is_same<T, float>::value) store8(out + m * ld + n, v, cols - n, vec);
-      else store8<T>(out + m * ld + n, v, cols - n, vec);
-    }
-  }
 }
 
 // dx = [dg du] [Wg; Wu]: k runs along the rows of the weights.
@@ -399,9 +385,9 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dx_kernel(con
   multiply<T, G, kRows, kCols>(lds[team], steps, mrow, ncol, ncol + S / G::WN / 2, at_step, issue, [](char*) {}, acc);
   add_teams<KG, G::NW>(lds, team, wave, acc);
   if (p.splits == 1)
-    store_tile<T, G>(lds[0][0] + wave * kRowScratch<G::NT / 2>, p.dx, p.lddx, p.rows, p.d, m0, mrow, n0 + ncol, team, p.vec, acc);
+    store_tile<T, G>(lds[0][0], p.dx, p.lddx, p.rows, p.d, m0, mrow, n0 + ncol, team, wave, p.vec, acc);
   else
-    store_tile<float, G>(nullptr, p.parts + blockIdx.y * p.rows * p.d, p.d, p.rows, p.d, m0, mrow, n0 + ncol, team, p.d % 4 == 0, acc);
+    store_tile<float, G>(lds[0][0], p.parts + blockIdx.y * p.rows * p.d, p.d, p.rows, p.d, m0, mrow, n0 + ncol, team, wave, p.d % 4 == 0, acc);
 #endif
 }
 
@@ -446,7 +432,7 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dw_kernel(con
   f32x4 acc[G::MT][G::NT];
   multiply<T, G, kCols, kCols>(lds[team], steps, mrow, ncol, ncol + S / G::WN / 2, at_step, issue, [](char*) {}, acc);
   add_teams<KG, G::NW>(lds, team, wave, acc);
-  store_tile<T, G>(lds[0][0] + wave * kRowScratch<G::NT / 2>, second ? p.dwu : p.dwg, p.lddw, p.f, p.d, f0, mrow, n0 + ncol, team, p.vec, acc);
+  store_tile<T, G>(lds[0][0], second ? p.dwu : p.dwg, p.lddw, p.f, p.d, f0, mrow, n0 + ncol, team, wave, p.vec, acc);
 #endif
 }
 

@@ -465,29 +465,43 @@ __device__ __forceinline__ void store8(uint16_t* p, const float* v, int64_t left
 // 16 rows (matrix tile j of the wave's) of NG 32-column groups, through LDS, so
 // that a store instruction writes whole rows of 64*NG bytes: straight from the
 // fragments it would write 64 bytes of each of 16 rows, half cache lines (3 x 268
-// MB in 205 us more than one of them alone; so 2.6 TB/s).  Only the wave itself reads
-// what it wrote, and LDS keeps a wave's order.
+// MB in 205 us more than one of them alone; so in 110).  `left` columns exist from
+// out on; vec: 16 bytes may be stored at once, else each lane stores an element
+// beside its neighbour's (an odd distance between rows).  Only the wave itself
+// reads what it wrote, and LDS keeps a wave's order.
 template <int NG> constexpr int kRowScratch = 16 * NG * 64;
 template <class T, int NG>
-__device__ __forceinline__ void store_rows(char* scratch, uint16_t* out, int64_t ld, int64_t rows, int64_t m0, int mrow, int j,
-                                           const float (&v)[NG][8]) {
+__device__ __forceinline__ void store_rows(char* scratch, uint16_t* out, int64_t ld, int64_t rows, int left, bool vec,
+                                           int64_t m0, int mrow, int j, const float (&v)[NG][8]) {
   constexpr int kChunks = 4 * NG;      // of 16 bytes in a row
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  auto place = [](int row, int chunk) { return (row * kChunks + (chunk ^ (row & (kChunks - 1)))) * 16; };
+  auto row_at = [&](int row) { return m0 + mrow + (j >> 1) * 32 + 4 * (j & 1) + 8 * (row >> 2) + (row & 3); };
 #pragma unroll
   for (int q = 0; q < NG; ++q) {
     i32x4 w;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       w[i] = static_cast<int>(bits_of(T{}, v[q][2 * i]) | (bits_of(T{}, v[q][2 * i + 1]) << 16));
-    *reinterpret_cast<i32x4*>(scratch + (r * kChunks + ((4 * q + g) ^ (r & (kChunks - 1)))) * 16) = w;
+    *reinterpret_cast<i32x4*>(scratch + place(r, 4 * q + g)) = w;
   }
   __builtin_amdgcn_wave_barrier();
+  if (vec && left >= 32 * NG) {
 #pragma unroll
-  for (int n = 0; n < 16 * kChunks / 64; ++n) {
-    const int row = (n * 64 + lane) / kChunks, chunk = (n * 64 + lane) % kChunks;
-    const i32x4 w = *reinterpret_cast<const i32x4*>(scratch + (row * kChunks + (chunk ^ (row & (kChunks - 1)))) * 16);
-    const int64_t m = m0 + mrow + (j >> 1) * 32 + 4 * (j & 1) + 8 * (row >> 2) + (row & 3);
-    if (m < rows) *reinterpret_cast<i32x4*>(out + m * ld + chunk * 8) = w;
+    for (int n = 0; n < 16 * kChunks / 64; ++n) {
+      const int row = (n * 64 + lane) / kChunks, chunk = (n * 64 + lane) % kChunks;
+      const i32x4 w = *reinterpret_cast<const i32x4*>(scratch + place(row, chunk));
+      const int64_t m = row_at(row);
+      if (m < rows) *reinterpret_cast<i32x4*>(out + m * ld + chunk * 8) = w;
+    }
+  } else {
+#pragma unroll 4
+    for (int n = 0; n < 16 * 32 * NG / 64; ++n) {
+      const int row = (n * 64 + lane) / (32 * NG), col = (n * 64 + lane) % (32 * NG);
+      const uint16_t w = *reinterpret_cast<const uint16_t*>(scratch + place(row, col >> 3) + (col & 7) * 2);
+      const int64_t m = row_at(row);
+      if (m < rows && col < left) out[m * ld + col] = w;
+    }
   }
   __builtin_amdgcn_wave_barrier();
 }
