@@ -78,7 +78,7 @@ typedef struct opt8_fp8_quant {
   void* qt;            /* codes of x transposed [cols, rows], or NULL                 */
   float* scale_t;
   int64_t rows, cols;  /* >= 0; an empty x queues nothing                             */
-  int64_t ldx;         /* x: element alignment is enough, 16 bytes faster             */
+  int64_t ldx;         /* x: element alignment is enough                              */
   int64_t ldq, ldt;    /* multiples of 16                                             */
   int32_t x_type;      /* OPT8_TYPE_BF16, FP16 or FP32                                */
   int32_t q_type;      /* OPT8_TYPE_E4M3 or E5M2                                      */

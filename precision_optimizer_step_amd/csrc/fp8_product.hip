@@ -28,7 +28,6 @@ struct Product {
   int m, n, k;
   int nb;        // entries of sb for one block of k
   int tiles_m, tiles_n, band;
-  bool vec;      // C takes 16-byte stores
 };
 
 // (The body is for the device pass alone: the host pass of this compiler
@@ -229,7 +228,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Pro
       float v[NG][8];
 #pragma unroll
       for (int i = 0; i < NG; ++i) take8(acc, q + i, j, v[i]);
-      if (n < p.n) store_rows<C, NG>(scratch, p.c + n, p.ldc, p.m, p.n - n, p.vec, m0, wm * (BM / WM), j, v);
+      if (n < p.n) store_rows<C, NG>(scratch, p.c + n, p.ldc, p.m, p.n - n, m0, wm * (BM / WM), j, v);
     }
 #endif
 }
@@ -412,7 +411,6 @@ hipError_t launch_fp8_matmul(const opt8_fp8_product& q, hipStream_t stream) {
   p.k = static_cast<int>(q.k);
   p.nb = q.block_b == OPT8_FP8_BLOCK_TILE ? (p.n + 127) / 128 : p.n;
   p.tiles_m = p.tiles_n = p.band = 0;
-  p.vec = reinterpret_cast<uintptr_t>(q.c) % 16 == 0 && q.ldc % 8 == 0;
   if (q.a_type == OPT8_TYPE_E5M2) return launch_type<1>(p, q.c_type, q.block_b, stream);
   return launch_type<0>(p, q.c_type, q.block_b, stream);
 }

@@ -19,7 +19,6 @@ struct Quant {
   float* scale_t;
   int64_t rows, cols, ldx, ldq, ldt;
   int cb, rb;    // blocks of columns and of rows
-  bool vec;      // x takes 16-byte loads
 };
 
 template <class X> struct Raw { typedef uint16_t type; };
@@ -32,9 +31,9 @@ template <class X>
 struct Eight {
   i16x8 v;
   __device__ __forceinline__ void zero() { v = i16x8{0, 0, 0, 0, 0, 0, 0, 0}; }
-  __device__ __forceinline__ void load(const uint16_t* p, int64_t left, bool vec) {
-    if (vec && left >= 8) {
-      v = *reinterpret_cast<const i16x8*>(p);
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t left) {
+    if (left >= 8) {
+      v = __builtin_bit_cast(i16x8, static_cast<i32x4>(*reinterpret_cast<const i32x4_at2*>(p)));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i < left ? static_cast<short>(p[i]) : 0;
@@ -49,9 +48,9 @@ struct Eight<float> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
   }
-  __device__ __forceinline__ void load(const float* p, int64_t left, bool vec) {
-    if (vec && left >= 8) {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  __device__ __forceinline__ void load(const float* p, int64_t left) {
+    if (left >= 8) {
+      const f32x4 a = *reinterpret_cast<const f32x4_at4*>(p), b = *reinterpret_cast<const f32x4_at4*>(p + 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
     } else {
@@ -114,7 +113,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const Quant p) {
   const int64_t cleft = p.cols - c0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (r0 + i < p.rows && cleft > 0) v[i].load(x + (r0 + i) * p.ldx + c0, cleft, p.vec);
+    if (r0 + i < p.rows && cleft > 0) v[i].load(x + (r0 + i) * p.ldx + c0, cleft);
     else v[i].zero();
   }
 
@@ -247,8 +246,6 @@ hipError_t launch_fp8_quantize(const opt8_fp8_quant& a, hipStream_t stream) {
   p.ldt = a.ldt;
   p.cb = static_cast<int>((a.cols + 127) / 128);
   p.rb = static_cast<int>((a.rows + 127) / 128);
-  const int64_t size = a.x_type == OPT8_TYPE_FP32 ? 4 : 2;
-  p.vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * size % 16 == 0;
   if (a.x_type == OPT8_TYPE_BF16) return launch_format<Bf16>(p, a.q_type, a.block, stream);
   if (a.x_type == OPT8_TYPE_FP16) return launch_format<Fp16>(p, a.q_type, a.block, stream);
   return launch_format<float>(p, a.q_type, a.block, stream);

@@ -83,7 +83,6 @@ struct Forward {
   int64_t ldh, ldg;     // elements
   int rows, d, f, act;
   int tiles_m, tiles_n, band;
-  bool vec;
 };
 
 // A tile holds B/2 rows of Wg and the same rows of Wu beside B rows of x; a
@@ -149,10 +148,10 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_forward_kerne
 #pragma unroll
           for (int i = 0; i < 8; ++i) h[t][i] = activate<decltype(act)::value>(g[t][i]) * u[t][i];
         }
-        store_rows<T, NS>(scratch, p.h + n, p.ldh, p.rows, p.f - n, p.vec, m0, mrow, j, h);
+        store_rows<T, NS>(scratch, p.h + n, p.ldh, p.rows, p.f - n, m0, mrow, j, h);
         if (p.gate) {
-          store_rows<T, NS>(scratch, p.gate + n, p.ldg, p.rows, p.f - n, p.vec, m0, mrow, j, g);
-          store_rows<T, NS>(scratch, p.up + n, p.ldg, p.rows, p.f - n, p.vec, m0, mrow, j, u);
+          store_rows<T, NS>(scratch, p.gate + n, p.ldg, p.rows, p.f - n, m0, mrow, j, g);
+          store_rows<T, NS>(scratch, p.up + n, p.ldg, p.rows, p.f - n, m0, mrow, j, u);
         }
       }
   });
@@ -273,7 +272,6 @@ struct Backward {
   int64_t lddh, ldg, lddx, lddw;
   int d, f, act;
   int tiles_m, tiles_n, band;
-  bool vec;
 };
 
 // dg and du, rounded to the type that the products take, zeros in the columns
@@ -313,8 +311,8 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(const Backward p) {
       }
     });
     uint16_t* o = reinterpret_cast<uint16_t*>(p.both) + m * 2 * p.width + n;
-    store8<T>(o, dg, 8, true);
-    store8<T>(o + p.width, du, 8, true);
+    *reinterpret_cast<i32x4*>(o) = packed<T>(dg);
+    *reinterpret_cast<i32x4*>(o + p.width) = packed<T>(du);
   }
 }
 
@@ -322,7 +320,7 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(const Backward p) {
 // of several teams each stores its share.
 template <class T, class G, class Out>
 __device__ __forceinline__ void store_tile(char* copies, Out* out, int64_t ld, int64_t rows, int cols, int64_t m0, int mrow,
-                                           int n0, int team, int wave, bool vec, const f32x4 (&acc)[G::MT][G::NT]) {
+                                           int n0, int team, int wave, const f32x4 (&acc)[G::MT][G::NT]) {
   constexpr int NG = G::NT / 2, KG = G::kTeams, NS = KG == 1 ? NG : 1;
   char* scratch = copies + (team * G::NW + wave) * kRowScratch<NS>;
   __syncthreads();       // other waves may still read what the results are staged in
@@ -340,13 +338,13 @@ __device__ __forceinline__ void store_tile(char* copies, Out* out, int64_t ld, i
         for (int t = 0; t < NS; ++t) {
           float v[8];
           take8(acc, q + t, j, v);
-          if (m < rows) store8(out + m * ld + at + 32 * t, v, cols - at - 32 * t, vec);
+          if (m < rows) store_some(out + m * ld + at + 32 * t, v, cols - at - 32 * t);
         }
       } else {
         float v[NS][8];
 #pragma unroll
         for (int t = 0; t < NS; ++t) take8(acc, q + t, j, v[t]);
-        store_rows<T, NS>(scratch, out + n, ld, rows, cols - n, vec, m0, mrow, j, v);
+        store_rows<T, NS>(scratch, out + n, ld, rows, cols - n, m0, mrow, j, v);
       }
     }
 }
@@ -385,9 +383,9 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dx_kernel(con
   multiply<T, G, kRows, kCols>(lds[team], steps, mrow, ncol, ncol + S / G::WN / 2, at_step, issue, [](char*) {}, acc);
   add_teams<KG, G::NW>(lds, team, wave, acc);
   if (p.splits == 1)
-    store_tile<T, G>(lds[0][0], p.dx, p.lddx, p.rows, p.d, m0, mrow, n0 + ncol, team, wave, p.vec, acc);
+    store_tile<T, G>(lds[0][0], p.dx, p.lddx, p.rows, p.d, m0, mrow, n0 + ncol, team, wave, acc);
   else
-    store_tile<float, G>(lds[0][0], p.parts + blockIdx.y * p.rows * p.d, p.d, p.rows, p.d, m0, mrow, n0 + ncol, team, wave, p.d % 4 == 0, acc);
+    store_tile<float, G>(lds[0][0], p.parts + blockIdx.y * p.rows * p.d, p.d, p.rows, p.d, m0, mrow, n0 + ncol, team, wave, acc);
 #endif
 }
 
@@ -432,11 +430,9 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dw_kernel(con
   f32x4 acc[G::MT][G::NT];
   multiply<T, G, kCols, kCols>(lds[team], steps, mrow, ncol, ncol + S / G::WN / 2, at_step, issue, [](char*) {}, acc);
   add_teams<KG, G::NW>(lds, team, wave, acc);
-  store_tile<T, G>(lds[0][0], second ? p.dwu : p.dwg, p.lddw, p.f, p.d, f0, mrow, n0 + ncol, team, wave, p.vec, acc);
+  store_tile<T, G>(lds[0][0], second ? p.dwu : p.dwg, p.lddw, p.f, p.d, f0, mrow, n0 + ncol, team, wave, acc);
 #endif
 }
-
-bool wide(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * 2 % 16 == 0; }
 
 // Microseconds that `tiles` tiles of `steps` steps take, `at_once` of them side by
 // side on the chip: a full round runs steps * step + fixed, a last round of at
@@ -507,7 +503,6 @@ hipError_t backward(Backward p, hipStream_t stream) {
     p.tiles_n = static_cast<int>((n + size - 1) / size);
   };
   if (p.dx && p.rows > 0) {
-    p.vec = wide(p.dx, p.lddx);
     with_tiling(p.rows, p.d, 2 * p.width / p.splits, p.splits, [&](auto g) {
       typedef decltype(g) G;
       cover(p.rows, p.d, G::kSize);
@@ -521,7 +516,6 @@ hipError_t backward(Backward p, hipStream_t stream) {
     }
   }
   if (p.dwg) {
-    p.vec = wide(p.dwg, p.lddw) && wide(p.dwu, p.lddw);
     with_tiling(p.f, p.d, p.rows, 2, [&](auto g) {
       typedef decltype(g) G;
       cover(p.f, p.d, G::kSize);
@@ -553,7 +547,6 @@ hipError_t launch_gated_ffn_forward(const opt8_gated_ffn& a, hipStream_t stream)
   p.f = static_cast<int>(a.f);
   p.act = a.act;
   p.tiles_m = p.tiles_n = p.band = 0;
-  p.vec = wide(a.h, a.ldh) && (!a.gate || (wide(a.gate, a.ldg) && wide(a.up, a.ldg)));
   return a.type == OPT8_TYPE_BF16 ? forward<Bf16>(p, stream) : forward<Fp16>(p, stream);
 }
 
@@ -583,7 +576,6 @@ hipError_t launch_gated_ffn_backward(const opt8_gated_ffn_grad& a, hipStream_t s
   p.f = static_cast<int>(a.f);
   p.act = a.act;
   p.tiles_m = p.tiles_n = p.band = 0;
-  p.vec = false;
   return a.type == OPT8_TYPE_BF16 ? backward<Bf16>(p, stream) : backward<Fp16>(p, stream);
 }
 

@@ -446,70 +446,61 @@ template <class T> __device__ __forceinline__ float value_of(uint16_t b);
 template <> __device__ __forceinline__ float value_of<Bf16>(uint16_t b) { return static_cast<float>(__builtin_bit_cast(__bf16, b)); }
 template <> __device__ __forceinline__ float value_of<Fp16>(uint16_t b) { return static_cast<float>(__builtin_bit_cast(_Float16, b)); }
 
-// Stores 8 consecutive results, each rounded once (to nearest, ties to even);
-// `left` of them exist.  vec: the matrix lets 16 bytes be stored at once.
-template <class T>
-__device__ __forceinline__ void store8(uint16_t* p, const float* v, int64_t left, bool vec) {
-  if (vec && left >= 8) {
-    i32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = static_cast<int>(bits_of(T{}, v[2 * i]) | (bits_of(T{}, v[2 * i + 1]) << 16));
-    *reinterpret_cast<i32x4*>(p) = w;
+// Loads and stores of 16 bytes at any alignment of their elements: the hardware
+// splits those that cross a line (n = 10941 results a row: 139 us with an element
+// to a lane).
+typedef i32x4 __attribute__((aligned(2))) i32x4_at2;
+typedef f32x4 __attribute__((aligned(4))) f32x4_at4;
+
+// The first `left` (at most 8) of 8 results.
+__device__ __forceinline__ void store_some(uint16_t* p, i32x4 w, int64_t left) {
+  if (left >= 8) {
+    *reinterpret_cast<i32x4_at2*>(p) = w;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = static_cast<uint16_t>(bits_of(T{}, v[i]));
+      if (i < left) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
   }
+}
+// 8 results, each rounded once (to nearest, ties to even).
+template <class T>
+__device__ __forceinline__ i32x4 packed(const float* v) {
+  i32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = static_cast<int>(bits_of(T{}, v[2 * i]) | (bits_of(T{}, v[2 * i + 1]) << 16));
+  return w;
 }
 
 // 16 rows (matrix tile j of the wave's) of NG 32-column groups, through LDS, so
 // that a store instruction writes whole rows of 64*NG bytes: straight from the
 // fragments it would write 64 bytes of each of 16 rows, half cache lines (3 x 268
 // MB in 205 us more than one of them alone; so in 110).  `left` columns exist from
-// out on; vec: 16 bytes may be stored at once, else each lane stores an element
-// beside its neighbour's (an odd distance between rows).  Only the wave itself
-// reads what it wrote, and LDS keeps a wave's order.
+// out on.  Only the wave itself reads what it wrote, and LDS keeps a wave's order.
 template <int NG> constexpr int kRowScratch = 16 * NG * 64;
 template <class T, int NG>
-__device__ __forceinline__ void store_rows(char* scratch, uint16_t* out, int64_t ld, int64_t rows, int left, bool vec,
-                                           int64_t m0, int mrow, int j, const float (&v)[NG][8]) {
+__device__ __forceinline__ void store_rows(char* scratch, uint16_t* out, int64_t ld, int64_t rows, int left, int64_t m0,
+                                           int mrow, int j, const float (&v)[NG][8]) {
   constexpr int kChunks = 4 * NG;      // of 16 bytes in a row
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   auto place = [](int row, int chunk) { return (row * kChunks + (chunk ^ (row & (kChunks - 1)))) * 16; };
   auto row_at = [&](int row) { return m0 + mrow + (j >> 1) * 32 + 4 * (j & 1) + 8 * (row >> 2) + (row & 3); };
 #pragma unroll
-  for (int q = 0; q < NG; ++q) {
-    i32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = static_cast<int>(bits_of(T{}, v[q][2 * i]) | (bits_of(T{}, v[q][2 * i + 1]) << 16));
-    *reinterpret_cast<i32x4*>(scratch + place(r, 4 * q + g)) = w;
-  }
+  for (int q = 0; q < NG; ++q) *reinterpret_cast<i32x4*>(scratch + place(r, 4 * q + g)) = packed<T>(v[q]);
   __builtin_amdgcn_wave_barrier();
-  if (vec && left >= 32 * NG) {
 #pragma unroll
-    for (int n = 0; n < 16 * kChunks / 64; ++n) {
-      const int row = (n * 64 + lane) / kChunks, chunk = (n * 64 + lane) % kChunks;
-      const i32x4 w = *reinterpret_cast<const i32x4*>(scratch + place(row, chunk));
-      const int64_t m = row_at(row);
-      if (m < rows) *reinterpret_cast<i32x4*>(out + m * ld + chunk * 8) = w;
-    }
-  } else {
-#pragma unroll 4
-    for (int n = 0; n < 16 * 32 * NG / 64; ++n) {
-      const int row = (n * 64 + lane) / (32 * NG), col = (n * 64 + lane) % (32 * NG);
-      const uint16_t w = *reinterpret_cast<const uint16_t*>(scratch + place(row, col >> 3) + (col & 7) * 2);
-      const int64_t m = row_at(row);
-      if (m < rows && col < left) out[m * ld + col] = w;
-    }
+  for (int n = 0; n < 16 * kChunks / 64; ++n) {
+    const int row = (n * 64 + lane) / kChunks, chunk = (n * 64 + lane) % kChunks;
+    const i32x4 w = *reinterpret_cast<const i32x4*>(scratch + place(row, chunk));
+    const int64_t m = row_at(row);
+    if (m < rows) store_some(out + m * ld + chunk * 8, w, left - chunk * 8);
   }
   __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ void store8(float* p, const float* v, int64_t left, bool vec) {
-  if (vec && left >= 8) {
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+__device__ __forceinline__ void store_some(float* p, const float* v, int64_t left) {
+  if (left >= 8) {
+    *reinterpret_cast<f32x4_at4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4_at4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
