@@ -334,24 +334,17 @@ __global__ __launch_bounds__(256) void product_few_kernel(const Product p) {
 #endif
 }
 
-// Microseconds of one step (128 k) of a whole launch of `tiles` tiles, of which
-// `at_once` run side by side on the chip (256 CUs) and a part of at most `few` in
-// less time: `round` a full round takes, `short_round` such a part.
-double rounds(int64_t tiles, int at_once, double round, int few, double short_round) {
-  const int64_t rest = tiles % at_once;
-  return static_cast<double>(tiles / at_once) * round + (rest == 0 ? 0.0 : rest <= few ? short_round : round);
-}
-
-// The kernel is the one that the estimate below calls fastest.  Its constants
-// were measured at k = 4096 (us a step, n = 4096 unless named; TILE, and ROW
-// where it differs; the kernels from left to right):
-//              256x256    128x128   128x128, 2 teams   64x64, 2 teams   64x64, 4 teams
-//   m =  128     1.45       0.64          0.59              0.34             0.32
-//   m =  512     1.54       0.77          0.66              0.52             0.70
-//   m = 1024     1.57       0.83          0.74              0.97             1.38
-//   m = 2048     1.66       1.15          1.45              1.83             2.66
-//   m = 4096     1.96/2.36  2.19/2.50     2.74              3.57             5.12
-//   8192^2       7.7/9.6    8.8/10.2      10.9              14.2             20.3
+// The kernel is the one that the estimate calls fastest.  Its constants fit these
+// measurements (us at n = 4096, k = 4096 unless named; TILE, and ROW where it
+// differs; the kernels from left to right):
+//                     256x256    128x128   128x128, 2 teams   64x64, 2 teams   64x64, 4 teams
+//   m =  128             43         21           19                10.8             10.4
+//   m =  512             44         25           21                17.1             23
+//   m = 1024             46         27           25                32               47
+//   m = 2048             50/66      38/43        48                62               90
+//   m = 4096             62/75      74/83        96               119              174
+//   8192 x 8192         244/299    286/327      356               466              670
+//   8192 x 8192, k 512   56         65          107               128              300
 // At most 16 rows go to the kernel without LDS (k = 16384, one row: 12.5 us
 // against 30.5 of the 64x64 tiles; 16 rows: 17.3 against 31.0; but n = 16384, k =
 // 4096, 16 rows: 16.7 against 14.9).
@@ -362,12 +355,13 @@ hipError_t launch(Product p, hipStream_t stream) {
     return hipGetLastError();
   }
   auto tiles = [&](int size) { return static_cast<int64_t>((p.m + size - 1) / size) * ((p.n + size - 1) / size); };
+  const int64_t steps = (p.k + kStepBytes - 1) / kStepBytes;
   const double cost[5] = {
-      rounds(tiles(256), 256, TILE ? 2.0 : 2.4, 0, 0),
-      rounds(tiles(128), 512, TILE ? 1.12 : 1.26, 256, 0.80),
-      rounds(tiles(128), 256, 0.72, 0, 0),
-      rounds(tiles(64), 512, 0.53, 256, 0.34),
-      rounds(tiles(64), 256, 0.31, 0, 0),
+      estimate(tiles(256), steps, 256, TILE ? 1.9 : 2.3, 4, TILE ? 1.45 : 1.95, 4),
+      estimate(tiles(128), steps, 512, TILE ? 1.12 : 1.26, 3, 0.78, 3),
+      estimate(tiles(128), steps, 256, 0.70, 3, 0.68, 3),
+      estimate(tiles(64), steps, 512, 0.50, 1.5, 0.32, 1.5),
+      estimate(tiles(64), steps, 256, 0.29, 1.5, 0.28, 1.5),
   };
   const int best = static_cast<int>(std::min_element(cost, cost + 5) - cost);
   const int size = best == 0 ? 256 : best < 3 ? 128 : 64;

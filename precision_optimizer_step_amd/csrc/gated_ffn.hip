@@ -434,33 +434,23 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dw_kernel(con
 #endif
 }
 
-// Microseconds that `tiles` tiles of `steps` steps take, `at_once` of them side by
-// side on the chip: a full round runs steps * step + fixed, a last round of at
-// most 256 tiles (one to a CU) steps * step_few + fixed_few.
-double estimate(int64_t tiles, int64_t steps, int at_once, double step, double fixed, double step_few, double fixed_few) {
-  const int64_t rest = tiles % at_once;
-  const double full = static_cast<double>(steps) * step + fixed;
-  const double last = rest == 0 ? 0.0 : rest <= 256 ? static_cast<double>(steps) * step_few + fixed_few : full;
-  return static_cast<double>(tiles / at_once) * full + last;
-}
-
 // Calls f with the tiling that covers `products` results of m x n, k long, in the
-// least time by the estimate, and with the tiles that gives.  The constants fit
-// these measurements (us; dx is m x n = rows x d, k = 2f):
+// least time by the estimate.  The constants fit these measurements (us; dx is m x
+// n = rows x d, k = 2f):
 //                                     256     128   128x2 teams  64x2   64x4
-//   dx   500 x 1024, k  8192          178      84        65       46     36
-//   dx  2048 x 1024, k  8192          177      85        67       54     74
-//   dx  2048 x 2560, k 20480          445     269       342      385    523
-//   dx  4096 x 4096, k  8192          206     254       281      389    558
-//   dw  8192 x 1024, k   500           22      15        20       28     43
-//   h    500 x 8192, k  1024           30      15        14       19     28
-//   h   8192 x 32768, k 4096         1784    2094      3089     3940   5942
+//   dx   500 x 1024, k  8192          151      84        65       48     38
+//   dx  2048 x 1024, k  8192          152      86        68       57     78
+//   dx  2048 x 2560, k 20480          366     251       350      395    531
+//   dx  4096 x 4096, k  8192          195     242       288      414    577
+//   dw  8192 x 1024, k   500           21      15        19       28     45
+//   h    500 x 8192, k  1024           28      14        14       19     30
+//   h   8192 x 32768, k 4096         1641    2134      3074     3956   6194
 template <class F>
 void with_tiling(int64_t m, int64_t n, int64_t k, int64_t products, F&& f) {
   auto tiles = [&](int64_t size) { return products * ((m + size - 1) / size) * ((n + size - 1) / size); };
   const int64_t steps = (k + 63) / 64;
   const double cost[5] = {
-      estimate(tiles(256), steps, 256, 1.65, 12, 1.45, 12),
+      estimate(tiles(256), steps, 256, 1.5, 11, 1.3, 11),
       estimate(tiles(128), steps, 512, 0.97, 7, 0.66, 5),
       estimate(tiles(128), steps, 256, 0.52, 6, 0.50, 6),
       estimate(tiles(64), steps, 512, 0.40, 3.5, 0.34, 3),

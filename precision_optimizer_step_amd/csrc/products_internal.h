@@ -37,4 +37,14 @@ inline int64_t gated_workspace(int64_t rows, int64_t d, int64_t f) {
   return gated_bytes(rows, f) + (splits > 1 ? splits * ((rows * d + 3) / 4 * 4) * 4 : 0);
 }
 
+// Microseconds that `tiles` tiles of `steps` steps take, `at_once` of them side by
+// side on the chip: a full round runs steps * step + fixed, a last round of at
+// most 256 tiles (one to a CU) steps * step_few + fixed_few.
+inline double estimate(int64_t tiles, int64_t steps, int at_once, double step, double fixed, double step_few, double fixed_few) {
+  const int64_t rest = tiles % at_once;
+  const double full = static_cast<double>(steps) * step + fixed;
+  const double last = rest == 0 ? 0.0 : rest <= 256 ? static_cast<double>(steps) * step_few + fixed_few : full;
+  return static_cast<double>(tiles / at_once) * full + last;
+}
+
 }  // namespace opt8
