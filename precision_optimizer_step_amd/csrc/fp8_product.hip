@@ -37,6 +37,12 @@ struct Product {
 // in LDS beside its operand tiles, one for each row of either (TILE scales are
 // spread over their rows by the loads' addresses).
 //
+// Every block's partial sums pass the vector ALU (4 fused multiply-adds a matrix
+// instruction with TILE scales, and 4 products more with ROW ones), which cannot
+// use accumulation registers: hence 128 x 64 results to a wave and two waves a
+// SIMD.  8192 x 16384 x 4096, TILE: 479 us, 2.29 PFLOP/s, matrix core 61% busy at
+// 1.8 GHz, a third of the waves' cycles at the barrier.
+//
 // KG > 1: KG teams of WM x WN waves share the tile's steps in turn, each with its
 // own copies, and add their sums through LDS at the end, in a fixed order: for
 // results too small to give every CU a tile.
