@@ -127,10 +127,10 @@ int quantize(const opt8_fp8_quant* a, void* hip_stream) {
   if (a->q_type != OPT8_TYPE_E4M3 && a->q_type != OPT8_TYPE_E5M2)
     return refuse(OPT8_E_MODE, "codes are e4m3 or e5m2 (got type %d)", a->q_type);
   if ((rc = check_block(a->block))) return rc;
+  if (a->rows == 0 || a->cols == 0) return OPT8_OK;
   if (!a->q && !a->qt) return refuse(OPT8_E_NULL, "q and qt are both NULL");
   if (!a->q != !a->scale) return refuse(OPT8_E_NULL, "q and scale go together");
   if (!a->qt != !a->scale_t) return refuse(OPT8_E_NULL, "qt and scale_t go together");
-  if (a->rows == 0 || a->cols == 0) return OPT8_OK;
   if (!a->x) return refuse(OPT8_E_NULL, "x is NULL");
   const bool tile = a->block == OPT8_FP8_BLOCK_TILE;
   const int64_t across = tile ? blocks(a->rows) : a->rows, across_t = tile ? blocks(a->cols) : a->cols;
@@ -181,8 +181,8 @@ int gated_forward(const opt8_gated_ffn* a, void* hip_stream) {
   if ((rc = check_count("rows", a->rows, 0, kMaxCount)) || (rc = check_count("d", a->d, 1, kMaxWidth)) ||
       (rc = check_count("f", a->f, 1, kMaxWidth)) || (rc = check_ffn_type(a->type, a->act)))
     return rc;
-  if (!a->gate != !a->up) return refuse(OPT8_E_NULL, "gate and up go together");
   if (a->rows == 0) return OPT8_OK;
+  if (!a->gate != !a->up) return refuse(OPT8_E_NULL, "gate and up go together");
   if (!a->x || !a->w_gate || !a->w_up || !a->h) return refuse(OPT8_E_NULL, "x, w_gate, w_up or h is NULL");
   const Matrix list[] = {
       {"x", a->x, a->rows, a->d, a->ldx, 2, false, true},
@@ -204,8 +204,9 @@ int gated_backward(const opt8_gated_ffn_grad* a, void* hip_stream) {
       (rc = check_count("f", a->f, 1, kMaxWidth)) || (rc = check_ffn_type(a->type, a->act)))
     return rc;
   if (!a->dw_gate != !a->dw_up) return refuse(OPT8_E_NULL, "dw_gate and dw_up go together");
-  if (!a->dx && !a->dw_gate) return refuse(OPT8_E_NULL, "dx and both dw are NULL");
   const bool some = a->rows > 0;
+  if (!some && !a->dw_gate) return OPT8_OK;
+  if (!a->dx && !a->dw_gate) return refuse(OPT8_E_NULL, "dx and both dw are NULL");
   if (some && (!a->dh || !a->gate || !a->up || !a->workspace || (a->dx && (!a->w_gate || !a->w_up)) || (a->dw_gate && !a->x)))
     return refuse(OPT8_E_NULL, "dh, gate, up, workspace, the weights (for dx) or x (for the dw) is NULL");
   const int64_t need = opt8_gated_ffn_workspace(a->rows, a->d, a->f);

@@ -395,3 +395,26 @@ def test_two_streams_at_once():
             ops.opt8_fp8_matmul(ops.make_fp8_product(a, sa, b, sb, c), stream=side)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(alone, outs))
+
+
+@pytest.mark.parametrize("rows,cols", [(0, 5), (5, 0), (0, 0)])
+def test_quantize_of_nothing(rows, cols):
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    for block in (ROW, TILE):
+        run_quantize(x, E4, block)
+
+
+def test_the_longest_rows():
+    """k at its limit (2^22), and rows 2^23 bytes apart: the last tile row's offsets end below 2^31."""
+    check_exact(2, 17, 1 << 22, seed=1)
+    check_exact(20, 17, 1 << 22, seed=2)
+    far, m, k = 1 << 23, 270, 300
+    store = torch.zeros(m, far, dtype=torch.uint8, device="cuda")
+    a = store.view(E4)[:, :k]
+    a.copy_(torch.randint(-1, 2, (m, k), generator=gen(3)).float().to(E4))
+    b = torch.randint(-1, 2, (40, 304), generator=gen(4)).float().to(E4).cuda()[:, :k]
+    c = torch.empty(m, 40, dtype=torch.bfloat16, device="cuda")
+    sa, sb = torch.ones(3, m, device="cuda"), torch.ones(3, 1, device="cuda")
+    ops.opt8_fp8_matmul(ops.make_fp8_product(a, sa, b, sb, c))
+    torch.cuda.synchronize()
+    assert torch.equal(c.double().cpu(), a.float().double().cpu() @ b.float().double().cpu().t())

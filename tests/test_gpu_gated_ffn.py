@@ -227,6 +227,9 @@ def test_backward_of_no_rows_clears_the_weights_gradients():
     ops.opt8_gated_ffn_backward(ops.make_gated_ffn_grad(n, e, w, w, n, n, e.clone(), a, b,
                                                         torch.empty(0, dtype=torch.uint8, device="cuda")))
     ops.opt8_gated_ffn_forward(ops.make_gated_ffn(e, w, w, n.clone()))
+    ops.opt8_gated_ffn_backward(ops.make_gated_ffn_grad(n, e, w, w, n, n, e.clone(), None, None,
+                                                        torch.empty(0, dtype=torch.uint8, device="cuda")))
+    ops.opt8_gated_ffn_forward(ops.make_gated_ffn(e, w, w, n.clone(), n.clone(), n.clone()))
     torch.cuda.synchronize()
     assert bool((a == 0).all()) and bool((b == 0).all())
 
