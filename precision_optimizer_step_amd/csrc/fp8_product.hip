@@ -92,8 +92,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Pro
   constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW, kAll = kA + kB + 1;
   // With one workgroup to a CU (256 x 256), the loads of a step are more than the
   // CU's cache path takes (64 bytes a cycle) in the two rows behind the barrier,
-  // and waves that wait to issue one stand still: some go to the next two rows.
-  constexpr int kLater = MT == 8 ? 4 : 0, kNow = kAll - kLater;
+  // and waves that wait to issue one stand still: some go to the next row (ROW, whose
+  // rows last longer, 2: 120 us against 127 with 4 in the weight gradient's case).
+  constexpr int kLater = MT == 8 ? (TILE ? 4 : 2) : 0, kNow = kAll - kLater;
   const uint32_t copies = lds_address(lds);
   auto issue = [&](uint32_t to, int l) {
     if (l < kA) la.issue(to, l);
@@ -171,8 +172,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void product_kernel(const Pro
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         constexpr bool two = MT == 2;     // both rows are read at the end of the step before
-        if (kLater && j < 2 && (4 * j + q) % 2 == 1)      // what was left of the next step's loads
-          issue(copies + ((step + 1) & 1) * kCopy, kNow + (4 * j + q) / 2);
+        if (j == 0 && q * kLater % 4 == 0 && kLater)      // what was left of the next step's loads
+          issue(copies + ((step + 1) & 1) * kCopy, kNow + q * kLater / 4);
         if (!two && j < MT - 2) {
           if (q == 0) read_a(step, j + 1);
           if (q == 2 && j == MT - 3) read_a(step, MT - 1);
