@@ -94,7 +94,7 @@ def _matrix(what, t, dtypes, rows, cols, owned=False):
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: dtype {t.dtype} not allowed here (expected one of "
                          f"{', '.join(str(d) for d in dtypes)})")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
     step, unit = t.stride()
     if cols > 1 and unit != 1:
@@ -107,7 +107,8 @@ def _matrix(what, t, dtypes, rows, cols, owned=False):
         step = -(-cols // each) * each if owned else cols
     if owned and rows and cols:
         each = 16 // t.element_size()
-        if t.storage_offset() + (rows - 1) * step + -(-cols // each) * each > t.untyped_storage().nbytes() // t.element_size():
+        end = t.storage_offset() + (rows - 1) * step + -(-cols // each) * each
+        if end > t.untyped_storage().nbytes() // t.element_size():
             raise ValueError(f"{what}: its storage ends inside the last 16 bytes of the last row")
     return step
 
@@ -115,22 +116,22 @@ def _matrix(what, t, dtypes, rows, cols, owned=False):
 def _scales(what, t, blocks, across):
     if t.dtype != torch.float32:
         raise ValueError(f"{what}: dtype {t.dtype} not allowed here (expected torch.float32)")
-    if tuple(t.shape) != (blocks, across):
+    if t.shape != (blocks, across):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected ({blocks}, {across})")
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
 
 
-def _placed(*tensors):
+def _placed(names, tensors):
     """All on one GPU, and that one current (a call queues on the current device)."""
-    first = tensors[0][1].get_device()
-    for what, t in tensors:
+    first = tensors[0].get_device()
+    for i, t in enumerate(tensors):
         if t is not None and t.get_device() != first:
-            raise ValueError(f"{what}: on {t.device}, but {tensors[0][0]} is on {tensors[0][1].device}")
+            raise ValueError(f"{names[i]}: on {t.device}, but {names[0]} is on {tensors[0].device}")
     if first < 0:
-        raise ValueError(f"{tensors[0][0]}: on {tensors[0][1].device}; the operators run on a GPU")
+        raise ValueError(f"{names[0]}: on {tensors[0].device}; the operators run on a GPU")
     if first != torch.cuda.current_device():
-        raise ValueError(f"{tensors[0][0]}: on cuda:{first}, but the current device is cuda:{torch.cuda.current_device()}")
+        raise ValueError(f"{names[0]}: on cuda:{first}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _ceil(n):
@@ -175,7 +176,7 @@ def make_fp8_quant(x, q=None, scale=None, qt=None, scale_t=None, block=OPT8_FP8_
             ldq = ld
         else:
             ldt = ld
-    _placed(("x", x), ("q", q), ("scale", scale), ("qt", qt), ("scale_t", scale_t))
+    _placed(("x", "q", "scale", "qt", "scale_t"), (x, q, scale, qt, scale_t))
     return opt8_fp8_quant(x.data_ptr(), _ptr(q), _ptr(scale), _ptr(qt), _ptr(scale_t), rows, cols, ldx, ldq, ldt,
                           _TYPE[x.dtype], _TYPE[kind], block)
 
@@ -193,7 +194,7 @@ def make_fp8_product(a, scale_a, b, scale_b, c, block_b=OPT8_FP8_BLOCK_TILE) -> 
     ldc = _matrix("c", c, _HALF, m, n)
     _scales("scale_a", scale_a, _ceil(k), m)
     _scales("scale_b", scale_b, _ceil(k), _ceil(n) if block_b == OPT8_FP8_BLOCK_TILE else n)
-    _placed(("a", a), ("scale_a", scale_a), ("b", b), ("scale_b", scale_b), ("c", c))
+    _placed(("a", "scale_a", "b", "scale_b", "c"), (a, scale_a, b, scale_b, c))
     return opt8_fp8_product(a.data_ptr(), scale_a.data_ptr(), b.data_ptr(), scale_b.data_ptr(), c.data_ptr(), m, n, k,
                             lda, ldb, ldc, _TYPE[a.dtype], _TYPE[b.dtype], _TYPE[c.dtype], block_b)
 
@@ -226,7 +227,7 @@ def make_gated_ffn(x, w_gate, w_up, h, gate=None, up=None, act=OPT8_ACT_SILU) ->
         ldg = _matrix("gate", gate, kind, rows, f)
         if _matrix("up", up, kind, rows, f) != ldg:
             raise ValueError("gate and up have different row distances")
-    _placed(("x", x), ("w_gate", w_gate), ("w_up", w_up), ("h", h), ("gate", gate), ("up", up))
+    _placed(("x", "w_gate", "w_up", "h", "gate", "up"), (x, w_gate, w_up, h, gate, up))
     return opt8_gated_ffn(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(), _ptr(gate), _ptr(up), rows, d,
                           f, ldx, ldw, ldh, ldg, _TYPE[x.dtype], act)
 
@@ -254,8 +255,8 @@ def make_gated_ffn_grad(dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, works
             raise ValueError("dw_gate and dw_up have different row distances")
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous torch.uint8")
-    _placed(("x", x), ("dh", dh), ("w_gate", w_gate), ("w_up", w_up), ("gate", gate), ("up", up), ("dx", dx),
-            ("dw_gate", dw_gate), ("dw_up", dw_up), ("workspace", workspace))
+    _placed(("x", "dh", "w_gate", "w_up", "gate", "up", "dx", "dw_gate", "dw_up", "workspace"),
+            (x, dh, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace))
     return opt8_gated_ffn_grad(dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(),
                                up.data_ptr(), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), workspace.data_ptr(),
                                workspace.numel(), rows, d, f, ldx, ldw, lddh, ldg, lddx, lddw, _TYPE[x.dtype], act)
@@ -275,8 +276,8 @@ def _current_stream():
 
 
 def _call(name, desc, stream, check):
-    rc = _functions()[name](desc, (_current_stream() if stream is None else _stream_handle(stream)) or None)
-    return _check(rc) if check else rc
+    rc = (_fns or _functions())[name](desc, (_current_stream() if stream is None else _stream_handle(stream)) or None)
+    return _check(rc) if check and rc else rc
 
 
 def opt8_fp8_quantize(quant: opt8_fp8_quant, stream=None, check: bool = True) -> int:
