@@ -54,7 +54,9 @@ __device__ __forceinline__ void activate(float g, float& value, float& slope) {
     const float y = kTanhA * g * __builtin_fmaf(kTanhB * g, g, 1.0f);
     const float p = sigmoid(2.0f * y);
     value = g * p;
-    slope = __builtin_fmaf(2.0f * g * p * (1.0f - p), kTanhA * __builtin_fmaf(3.0f * kTanhB * g, g, 1.0f), p);
+    // the bound keeps g*g finite beside the p(1 - p) = 0 of gates past 1e19
+    const float dy2 = __builtin_fminf(2.0f * kTanhA * __builtin_fmaf(3.0f * kTanhB * g, g, 1.0f), 0x1p127f);
+    slope = __builtin_fmaf(g * p * (1.0f - p), dy2, p);
   }
 }
 template <int ACT>
@@ -308,7 +310,7 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(const Backward p) {
         const float dh = value_of<T>(static_cast<uint16_t>(ra[i]));
         float value, slope;
         activate<decltype(act)::value>(value_of<T>(static_cast<uint16_t>(rb[i])), value, slope);
-        dg[i] = dh * value_of<T>(static_cast<uint16_t>(rc[i])) * slope;
+        dg[i] = dh * slope * value_of<T>(static_cast<uint16_t>(rc[i]));    // in this order: a slope of 0 stays 0
         du[i] = dh * value;
       }
     });

@@ -188,6 +188,30 @@ def test_backward_types_and_activations(dtype, act):
     check_backward(150, 96, 160, dtype, act, seed=4, extra=8)
 
 
+@pytest.mark.parametrize("act", list(ACT))
+def test_slopes_of_gates_whose_square_overflows(act):
+    """bf16 reaches past the square root of fp32's largest number: the slope is 0 or 1 there, and
+    a slope of 0 keeps dg at 0 where dh * u alone would overflow."""
+    far = [-3e38, -1e30, -1e20, -1e19, -1e15, -1e4, 1e4, 1e15, 1e19, 1e20, 1e30, 3e38]
+    gates = torch.tensor([far + [-1e4] * 4], dtype=BF)
+    ones = torch.ones_like(gates)
+    big = ones.clone()
+    big[:, 12:] = 1e20
+    f = gates.shape[1]
+    x = torch.zeros(1, 8, dtype=BF, device="cuda")
+    x[:, 0] = 1.0
+    w = torch.zeros(f, 8, dtype=BF, device="cuda")
+    dwg, dwu = torch.empty_like(w), torch.empty_like(w)
+    work = torch.empty(ops.opt8_gated_ffn_workspace(1, 8, f), dtype=torch.uint8, device="cuda")
+    ops.opt8_gated_ffn_backward(ops.make_gated_ffn_grad(big.cuda(), x, w, w.clone(), gates.cuda(), big.cuda(), None, dwg, dwu,
+                                                        work, act=ACT[act]))
+    torch.cuda.synchronize()
+    v, s = ref.act(gates.double(), act)
+    # slopes of exactly 0 or 1 and values of exactly 0 or g: every product is exact
+    assert torch.equal(dwg[:, 0].double().cpu(), s[0])
+    assert torch.equal(dwu[:, 0].double().cpu(), v[0])
+
+
 @pytest.mark.parametrize("dx,dw", [(True, False), (False, True)])
 def test_backward_of_one_side(dx, dw):
     check_backward(90, 64, 100, dx=dx, dw=dw, seed=5)
