@@ -19,8 +19,8 @@
  * 16 bytes of their last row whole (rows are read in pieces of 16 bytes; what
  * lies behind a row's end is ignored, and never written).  Other outputs need their
  * element's own alignment only and are faster on 16 bytes.  No count of rows
- * or columns exceeds 2^22 (d and f: 2^20), no matrix 2^37 elements, and no
- * ld*size of a matrix that feeds the matrix cores 2^23 bytes.  An output may
+ * or columns exceeds 2^22 (d and f: 2^20), no matrix 2^37 elements, no ld 2^38,
+ * and no ld*size of a matrix that feeds the matrix cores 2^23 bytes.  An output may
  * not overlap another buffer of the call; halves of one wider matrix (the same
  * ld, columns side by side) are apart, other spans that meet are refused.
  *

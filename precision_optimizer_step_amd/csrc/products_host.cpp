@@ -25,6 +25,7 @@ constexpr int64_t kMaxCount = int64_t{1} << 22;
 constexpr int64_t kMaxWidth = int64_t{1} << 20;
 constexpr int64_t kMaxElements = int64_t{1} << 37;
 constexpr int64_t kMaxRowBytes = int64_t{1} << 23;
+constexpr int64_t kMaxDistance = int64_t{1} << 38;    // of rows; kMaxCount of them span 2^62 bytes
 
 int type_bytes(int type) {
   switch (type) {
@@ -77,7 +78,7 @@ int check_matrices(const Matrix* list, int n) {
     if (x.ld < x.cols)
       return refuse(OPT8_E_SIZE, "%s: ld %lld is below its %lld columns", x.name, static_cast<long long>(x.ld),
                     static_cast<long long>(x.cols));
-    if (x.ld > (int64_t{1} << 40) || (x.core && x.ld * x.size > kMaxRowBytes))
+    if (x.ld > kMaxDistance || (x.core && x.ld * x.size > kMaxRowBytes))
       return refuse(OPT8_E_SIZE, "%s: ld %lld is too large", x.name, static_cast<long long>(x.ld));
     if (x.rows * x.cols > kMaxElements)
       return refuse(OPT8_E_SIZE, "%s: over 2^37 elements", x.name);

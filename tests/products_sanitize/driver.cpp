@@ -64,7 +64,7 @@ bool shared(const std::vector<Buffer>& list) {
 
 int failures = 0, accepted = 0, aliases = 0;
 
-void judge(int rc, int launches, const std::vector<Buffer>& list, const char* what) {
+void check(int rc, int launches, const std::vector<Buffer>& list, const char* what) {
   const bool ran = opt8::g_launches > launches;
   if (ran) {
     ++accepted;
@@ -104,7 +104,7 @@ void ffn(int round) {
   a.act = static_cast<int32_t>(upto(3));
   const int before = opt8::g_launches;
   const int rc = opt8_gated_ffn_forward(&a, nullptr);
-  judge(rc, before, {{h, a.rows, a.f, a.ldh, 2, true}, {g, a.rows, a.f, a.ldg, 2, true}, {u, a.rows, a.f, a.ldg, 2, true}},
+  check(rc, before, {{h, a.rows, a.f, a.ldh, 2, true}, {g, a.rows, a.f, a.ldg, 2, true}, {u, a.rows, a.f, a.ldg, 2, true}},
         "gated_ffn_forward");
 }
 
@@ -130,7 +130,7 @@ void quant(int round) {
   const int64_t na = tile ? 1 : a.rows, nt = tile ? 1 : a.cols;
   const int before = opt8::g_launches;
   const int rc = opt8_fp8_quantize(&a, nullptr);
-  judge(rc, before, {{x, a.rows, a.cols, a.ldx, xs, false}, {q, a.rows, a.cols, a.ldq, 1, true}, {s, 1, na, na, 4, true},
+  check(rc, before, {{x, a.rows, a.cols, a.ldx, xs, false}, {q, a.rows, a.cols, a.ldq, 1, true}, {s, 1, na, na, 4, true},
                      {qt, a.cols, a.rows, a.ldt, 1, true}, {st, 1, nt, nt, 4, true}}, "fp8_quantize");
 }
 
@@ -156,7 +156,7 @@ void product(int) {
   const int64_t nb = a.block_b == OPT8_FP8_BLOCK_TILE ? (a.n + 127) / 128 : a.n, kb = (a.k + 127) / 128;
   const int before = opt8::g_launches;
   const int rc = opt8_fp8_matmul(&a, nullptr);
-  judge(rc, before, {{c, a.m, a.n, a.ldc, 2, true}, {pa, a.k ? a.m : 0, a.k, a.lda, 1, false}, {sa, kb, a.m, a.m, 4, false},
+  check(rc, before, {{c, a.m, a.n, a.ldc, 2, true}, {pa, a.k ? a.m : 0, a.k, a.lda, 1, false}, {sa, kb, a.m, a.m, 4, false},
                      {pb, a.k ? a.n : 0, a.k, a.ldb, 1, false}, {sb, kb, nb, nb, 4, false}}, "fp8_matmul");
 }
 
@@ -184,7 +184,7 @@ void grad(int) {
   a.dw_up = at<void>(du);
   const int before = opt8::g_launches;
   const int rc = opt8_gated_ffn_backward(&a, nullptr);
-  judge(rc, before, {{dx, a.rows, a.d, a.lddx, 2, true}, {dg, a.f, a.d, a.lddw, 2, true}, {du, a.f, a.d, a.lddw, 2, true}},
+  check(rc, before, {{dx, a.rows, a.d, a.lddx, 2, true}, {dg, a.f, a.d, a.lddw, 2, true}, {du, a.f, a.d, a.lddw, 2, true}},
         "gated_ffn_backward");
 }
 
@@ -210,6 +210,17 @@ int main() {
       (void)opt8_gated_ffn_forward(&f, nullptr);
       (void)opt8_gated_ffn_workspace(v, w, v);
       (void)opt8_gated_ffn_workspace(w, v, v);
+    }
+  }
+  // the widest row distances beside the most rows: a matrix's span stays in 64 bits
+  for (int64_t ld : {int64_t{1} << 38, (int64_t{1} << 38) + 1, int64_t{1} << 40}) {
+    const int before = opt8::g_launches;
+    opt8_fp8_quant q{at<void>(1 << 20), at<void>(int64_t{1} << 62), at<float>(3 << 20), nullptr, nullptr, int64_t{1} << 22, 1, ld, 16, 0,
+                     OPT8_TYPE_FP32, OPT8_TYPE_E4M3, OPT8_FP8_BLOCK_TILE};
+    const int rc = opt8_fp8_quantize(&q, nullptr);
+    if (rc == OPT8_OK || opt8::g_launches != before) {
+      std::printf("ld %lld: scale lies in x's span, not refused\n", static_cast<long long>(ld));
+      ++failures;
     }
   }
   // a launch that fails is reported
