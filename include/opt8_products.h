@@ -147,7 +147,9 @@ typedef struct opt8_gated_ffn_grad {
   void* dx;
   void* dw_gate;
   void* dw_up;
-  void* workspace;     /* 16-byte aligned; contents need not be kept                  */
+  void* workspace;     /* 16-byte aligned; contents need not be kept.  The call writes it:
+                          calls that may run at once (on two streams, as replays of two
+                          captured graphs) take one each                              */
   int64_t workspace_bytes;
   int64_t rows, d, f;
   int64_t ldx, ldw;

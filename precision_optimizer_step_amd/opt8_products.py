@@ -236,7 +236,8 @@ def make_gated_ffn_grad(dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, works
                         act=OPT8_ACT_SILU) -> opt8_gated_ffn_grad:
     """Gradients of the block from dh [rows, f] and the stored gate and up: dx [rows, d]
     and dw_gate, dw_up [f, d] (dx, or both dw, may be None).  workspace: a contiguous
-    uint8 tensor of at least opt8_gated_ffn_workspace(rows, d, f) bytes."""
+    uint8 tensor of at least opt8_gated_ffn_workspace(rows, d, f) bytes, one for each call
+    that may run at the same time."""
     rows, d, f, kind, ldx, ldw = _weights(w_gate, w_up, x)
     lddh = _matrix("dh", dh, kind, rows, f, owned=True)
     ldg = _matrix("gate", gate, kind, rows, f, owned=True)
