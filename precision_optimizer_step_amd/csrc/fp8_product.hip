@@ -356,11 +356,8 @@ __global__ __launch_bounds__(256) void product_few_kernel(const Product p) {
 // against 30.5 of the 64x64 tiles; 16 rows: 17.3 against 31.0; but n = 16384, k =
 // 4096, 16 rows: 16.7 against 14.9).
 template <int FA, class C, bool TILE>
-hipError_t launch(Product p, hipStream_t stream) {
-  if (p.m <= 16) {
-    product_few_kernel<FA, C, TILE><<<(p.n + 15) / 16, 256, 0, stream>>>(p);
-    return hipGetLastError();
-  }
+hipError_t launch(Product& p, hipStream_t stream) {
+  if (p.m <= 16) return queue(product_few_kernel<FA, C, TILE>, (p.n + 15) / 16, 256, stream, p);
   auto tiles = [&](int size) { return static_cast<int64_t>((p.m + size - 1) / size) * ((p.n + size - 1) / size); };
   const int64_t steps = (p.k + kStepBytes - 1) / kStepBytes;
   const double cost[5] = {
@@ -376,21 +373,20 @@ hipError_t launch(Product p, hipStream_t stream) {
   p.tiles_n = (p.n + size - 1) / size;
   p.band = std::min(8, p.tiles_m);
   const unsigned grid = static_cast<unsigned>(tiles(size));
-  if (best == 0) product_kernel<FA, C, TILE, 256, 256, 2, 4><<<grid, 512, 0, stream>>>(p);
-  else if (best == 1) product_kernel<FA, C, TILE, 128, 128, 2, 2><<<grid, 256, 0, stream>>>(p);
-  else if (best == 2) product_kernel<FA, C, TILE, 128, 128, 2, 2, 2><<<grid, 512, 0, stream>>>(p);
-  else if (best == 3) product_kernel<FA, C, TILE, 64, 64, 2, 1, 2><<<grid, 256, 0, stream>>>(p);
-  else product_kernel<FA, C, TILE, 64, 64, 2, 1, 4><<<grid, 512, 0, stream>>>(p);
-  return hipGetLastError();
+  if (best == 0) return queue(product_kernel<FA, C, TILE, 256, 256, 2, 4>, grid, 512, stream, p);
+  if (best == 1) return queue(product_kernel<FA, C, TILE, 128, 128, 2, 2>, grid, 256, stream, p);
+  if (best == 2) return queue(product_kernel<FA, C, TILE, 128, 128, 2, 2, 2>, grid, 512, stream, p);
+  if (best == 3) return queue(product_kernel<FA, C, TILE, 64, 64, 2, 1, 2>, grid, 256, stream, p);
+  return queue(product_kernel<FA, C, TILE, 64, 64, 2, 1, 4>, grid, 512, stream, p);
 }
 
 template <int FA, class C>
-hipError_t launch_block(const Product& p, int block, hipStream_t stream) {
+hipError_t launch_block(Product& p, int block, hipStream_t stream) {
   return block == OPT8_FP8_BLOCK_TILE ? launch<FA, C, true>(p, stream) : launch<FA, C, false>(p, stream);
 }
 
 template <int FA>
-hipError_t launch_type(const Product& p, int type, int block, hipStream_t stream) {
+hipError_t launch_type(Product& p, int type, int block, hipStream_t stream) {
   if (type == OPT8_TYPE_BF16) return launch_block<FA, Bf16>(p, block, stream);
   return launch_block<FA, Fp16>(p, block, stream);
 }

@@ -217,16 +217,15 @@ __global__ __launch_bounds__(256) void quantize_kernel(const Quant p) {
 }
 
 template <class X, int F, bool TILE>
-hipError_t launch(const Quant& p, hipStream_t stream) {
+hipError_t launch(Quant& p, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(int64_t{p.cb} * p.rb);
-  if (p.q && p.qt) quantize_kernel<X, F, TILE, true, true><<<grid, 256, 0, stream>>>(p);
-  else if (p.q) quantize_kernel<X, F, TILE, true, false><<<grid, 256, 0, stream>>>(p);
-  else quantize_kernel<X, F, TILE, false, true><<<grid, 256, 0, stream>>>(p);
-  return hipGetLastError();
+  if (p.q && p.qt) return queue(quantize_kernel<X, F, TILE, true, true>, grid, 256, stream, p);
+  if (p.q) return queue(quantize_kernel<X, F, TILE, true, false>, grid, 256, stream, p);
+  return queue(quantize_kernel<X, F, TILE, false, true>, grid, 256, stream, p);
 }
 
 template <class X>
-hipError_t launch_format(const Quant& p, int format, int block, hipStream_t stream) {
+hipError_t launch_format(Quant& p, int format, int block, hipStream_t stream) {
   if (format == OPT8_TYPE_E4M3)
     return block == OPT8_FP8_BLOCK_TILE ? launch<X, 0, true>(p, stream) : launch<X, 0, false>(p, stream);
   return block == OPT8_FP8_BLOCK_TILE ? launch<X, 1, true>(p, stream) : launch<X, 1, false>(p, stream);

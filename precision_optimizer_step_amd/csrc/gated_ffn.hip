@@ -470,27 +470,26 @@ void with_tiling(int64_t m, int64_t n, int64_t k, int64_t products, F&& f) {
 }
 
 template <class T>
-hipError_t forward(Forward p, hipStream_t stream) {
-  if (p.rows <= 16) {
-    gated_forward_few_kernel<T><<<(p.f + 15) / 16, 256, 0, stream>>>(p);
-    return hipGetLastError();
-  }
+hipError_t forward(Forward& p, hipStream_t stream) {
+  if (p.rows <= 16) return queue(gated_forward_few_kernel<T>, (p.f + 15) / 16, 256, stream, p);
+  hipError_t e = hipSuccess;
   with_tiling(p.rows, 2 * int64_t{p.f}, p.d, 1, [&](auto g) {
     typedef decltype(g) G;
     p.tiles_m = (p.rows + G::kSize - 1) / G::kSize;
     p.tiles_n = (p.f + G::kSize / 2 - 1) / (G::kSize / 2);
     p.band = std::min(8, p.tiles_m);
-    gated_forward_kernel<T, G><<<p.tiles_m * p.tiles_n, G::kThreads, 0, stream>>>(p);
+    e = queue(gated_forward_kernel<T, G>, p.tiles_m * p.tiles_n, G::kThreads, stream, p);
   });
-  return hipGetLastError();
+  return e;
 }
 
 template <class T>
-hipError_t backward(Backward p, hipStream_t stream) {
+hipError_t backward(Backward& p, hipStream_t stream) {
+  hipError_t e = hipSuccess;
   const int64_t chunks = p.rows * (p.width / 8);
   if (chunks > 0) {
-    gated_slopes_kernel<T><<<static_cast<unsigned>(std::min<int64_t>((chunks + 255) / 256, 1 << 20)), 256, 0, stream>>>(p);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    e = queue(gated_slopes_kernel<T>, static_cast<unsigned>(std::min<int64_t>((chunks + 255) / 256, 1 << 20)), 256, stream, p);
+    if (e != hipSuccess) return e;
   }
   auto cover = [&](int64_t m, int64_t n, int size) {
     p.tiles_m = static_cast<int>((m + size - 1) / size);
@@ -501,12 +500,12 @@ hipError_t backward(Backward p, hipStream_t stream) {
       typedef decltype(g) G;
       cover(p.rows, p.d, G::kSize);
       p.band = std::min(8, p.tiles_m);
-      gated_dx_kernel<T, G><<<dim3(p.tiles_m * p.tiles_n, p.splits), G::kThreads, 0, stream>>>(p);
+      e = queue(gated_dx_kernel<T, G>, dim3(p.tiles_m * p.tiles_n, p.splits), G::kThreads, stream, p);
     });
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (e != hipSuccess) return e;
     if (p.splits > 1) {
-      gated_dx_sum_kernel<T><<<static_cast<unsigned>((p.rows * p.d + 255) / 256), 256, 0, stream>>>(p);
-      if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+      e = queue(gated_dx_sum_kernel<T>, static_cast<unsigned>((p.rows * p.d + 255) / 256), 256, stream, p);
+      if (e != hipSuccess) return e;
     }
   }
   if (p.dwg) {
@@ -515,11 +514,10 @@ hipError_t backward(Backward p, hipStream_t stream) {
       cover(p.f, p.d, G::kSize);
       p.tiles_m *= 2;
       p.band = std::min(8, p.tiles_m);
-      gated_dw_kernel<T, G><<<p.tiles_m * p.tiles_n, G::kThreads, 0, stream>>>(p);
+      e = queue(gated_dw_kernel<T, G>, p.tiles_m * p.tiles_n, G::kThreads, stream, p);
     });
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  return hipSuccess;
+  return e;
 }
 
 }  // namespace
