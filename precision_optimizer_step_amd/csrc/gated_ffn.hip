@@ -278,6 +278,14 @@ struct Backward {
   int tiles_m, tiles_n, band;
 };
 
+// dh * slope * up.  dh meets the slope first, so that a slope of 0 stays 0 where dh * up
+// overflows; where their product leaves fp32's normal numbers (bf16 gradients do with
+// saturated gates) the slope meets up instead, halved so that its 1.13 cannot overflow.
+__device__ __forceinline__ float slope_product(float dh, float slope, float up) {
+  const float first = dh * slope;
+  return __builtin_fabsf(first) < 0x1p-126f ? 0.5f * slope * up * dh * 2.0f : first * up;
+}
+
 // dg and du, rounded to the type that the products take, zeros in the columns
 // from f to width; 8 columns a thread.  8192 x 16384: 210 us, 1.34 GB at 6.4 TB/s.
 template <class T>
@@ -310,7 +318,7 @@ __global__ __launch_bounds__(256) void gated_slopes_kernel(const Backward p) {
         const float dh = value_of<T>(static_cast<uint16_t>(ra[i]));
         float value, slope;
         activate<decltype(act)::value>(value_of<T>(static_cast<uint16_t>(rb[i])), value, slope);
-        dg[i] = dh * slope * value_of<T>(static_cast<uint16_t>(rc[i]));    // in this order: a slope of 0 stays 0
+        dg[i] = slope_product(dh, slope, value_of<T>(static_cast<uint16_t>(rc[i])));
         du[i] = dh * value;
       }
     });
