@@ -38,25 +38,29 @@ _CODES = (torch.float8_e4m3fn, torch.float8_e5m2)
 _P, _L, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 
 
-class opt8_fp8_quant(ctypes.Structure):
+class _Descriptor(ctypes.Structure):
+    device = None     # index of the GPU that the tensors are on; None in a struct filled by hand
+
+
+class opt8_fp8_quant(_Descriptor):
     _fields_ = [("x", _P), ("q", _P), ("scale", _P), ("qt", _P), ("scale_t", _P),
                 ("rows", _L), ("cols", _L), ("ldx", _L), ("ldq", _L), ("ldt", _L),
                 ("x_type", _I), ("q_type", _I), ("block", _I)]
 
 
-class opt8_fp8_product(ctypes.Structure):
+class opt8_fp8_product(_Descriptor):
     _fields_ = [("a", _P), ("scale_a", _P), ("b", _P), ("scale_b", _P), ("c", _P),
                 ("m", _L), ("n", _L), ("k", _L), ("lda", _L), ("ldb", _L), ("ldc", _L),
                 ("a_type", _I), ("b_type", _I), ("c_type", _I), ("block_b", _I)]
 
 
-class opt8_gated_ffn(ctypes.Structure):
+class opt8_gated_ffn(_Descriptor):
     _fields_ = [("x", _P), ("w_gate", _P), ("w_up", _P), ("h", _P), ("gate", _P), ("up", _P),
                 ("rows", _L), ("d", _L), ("f", _L), ("ldx", _L), ("ldw", _L), ("ldh", _L), ("ldg", _L),
                 ("type", _I), ("act", _I)]
 
 
-class opt8_gated_ffn_grad(ctypes.Structure):
+class opt8_gated_ffn_grad(_Descriptor):
     _fields_ = [("dh", _P), ("x", _P), ("w_gate", _P), ("w_up", _P), ("gate", _P), ("up", _P),
                 ("dx", _P), ("dw_gate", _P), ("dw_up", _P), ("workspace", _P), ("workspace_bytes", _L),
                 ("rows", _L), ("d", _L), ("f", _L), ("ldx", _L), ("ldw", _L), ("lddh", _L), ("ldg", _L),
@@ -123,7 +127,7 @@ def _scales(what, t, blocks, across):
 
 
 def _placed(names, tensors):
-    """All on one GPU, and that one current (a call queues on the current device)."""
+    """The one GPU that all are on, and that one current (a call queues on the current device)."""
     first = tensors[0].get_device()
     for i, t in enumerate(tensors):
         if t is not None and t.get_device() != first:
@@ -132,6 +136,12 @@ def _placed(names, tensors):
         raise ValueError(f"{names[0]}: on {tensors[0].device}; the operators run on a GPU")
     if first != torch.cuda.current_device():
         raise ValueError(f"{names[0]}: on cuda:{first}, but the current device is cuda:{torch.cuda.current_device()}")
+    return first
+
+
+def _on(device, desc):
+    desc.device = device
+    return desc
 
 
 def _ceil(n):
@@ -176,9 +186,9 @@ def make_fp8_quant(x, q=None, scale=None, qt=None, scale_t=None, block=OPT8_FP8_
             ldq = ld
         else:
             ldt = ld
-    _placed(("x", "q", "scale", "qt", "scale_t"), (x, q, scale, qt, scale_t))
-    return opt8_fp8_quant(x.data_ptr(), _ptr(q), _ptr(scale), _ptr(qt), _ptr(scale_t), rows, cols, ldx, ldq, ldt,
-                          _TYPE[x.dtype], _TYPE[kind], block)
+    device = _placed(("x", "q", "scale", "qt", "scale_t"), (x, q, scale, qt, scale_t))
+    return _on(device, opt8_fp8_quant(x.data_ptr(), _ptr(q), _ptr(scale), _ptr(qt), _ptr(scale_t), rows, cols, ldx, ldq,
+                                      ldt, _TYPE[x.dtype], _TYPE[kind], block))
 
 
 def make_fp8_product(a, scale_a, b, scale_b, c, block_b=OPT8_FP8_BLOCK_TILE) -> opt8_fp8_product:
@@ -194,9 +204,9 @@ def make_fp8_product(a, scale_a, b, scale_b, c, block_b=OPT8_FP8_BLOCK_TILE) -> 
     ldc = _matrix("c", c, _HALF, m, n)
     _scales("scale_a", scale_a, _ceil(k), m)
     _scales("scale_b", scale_b, _ceil(k), _ceil(n) if block_b == OPT8_FP8_BLOCK_TILE else n)
-    _placed(("a", "scale_a", "b", "scale_b", "c"), (a, scale_a, b, scale_b, c))
-    return opt8_fp8_product(a.data_ptr(), scale_a.data_ptr(), b.data_ptr(), scale_b.data_ptr(), c.data_ptr(), m, n, k,
-                            lda, ldb, ldc, _TYPE[a.dtype], _TYPE[b.dtype], _TYPE[c.dtype], block_b)
+    device = _placed(("a", "scale_a", "b", "scale_b", "c"), (a, scale_a, b, scale_b, c))
+    return _on(device, opt8_fp8_product(a.data_ptr(), scale_a.data_ptr(), b.data_ptr(), scale_b.data_ptr(), c.data_ptr(), m,
+                                        n, k, lda, ldb, ldc, _TYPE[a.dtype], _TYPE[b.dtype], _TYPE[c.dtype], block_b))
 
 
 # ----------------------------------------------------------------------------- gated feed-forward block
@@ -227,9 +237,9 @@ def make_gated_ffn(x, w_gate, w_up, h, gate=None, up=None, act=OPT8_ACT_SILU) ->
         ldg = _matrix("gate", gate, kind, rows, f)
         if _matrix("up", up, kind, rows, f) != ldg:
             raise ValueError("gate and up have different row distances")
-    _placed(("x", "w_gate", "w_up", "h", "gate", "up"), (x, w_gate, w_up, h, gate, up))
-    return opt8_gated_ffn(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(), _ptr(gate), _ptr(up), rows, d,
-                          f, ldx, ldw, ldh, ldg, _TYPE[x.dtype], act)
+    device = _placed(("x", "w_gate", "w_up", "h", "gate", "up"), (x, w_gate, w_up, h, gate, up))
+    return _on(device, opt8_gated_ffn(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(), _ptr(gate), _ptr(up),
+                                      rows, d, f, ldx, ldw, ldh, ldg, _TYPE[x.dtype], act))
 
 
 def make_gated_ffn_grad(dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace,
@@ -256,11 +266,12 @@ def make_gated_ffn_grad(dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, works
             raise ValueError("dw_gate and dw_up have different row distances")
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous torch.uint8")
-    _placed(("x", "dh", "w_gate", "w_up", "gate", "up", "dx", "dw_gate", "dw_up", "workspace"),
-            (x, dh, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace))
-    return opt8_gated_ffn_grad(dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(),
-                               up.data_ptr(), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), workspace.data_ptr(),
-                               workspace.numel(), rows, d, f, ldx, ldw, lddh, ldg, lddx, lddw, _TYPE[x.dtype], act)
+    device = _placed(("x", "dh", "w_gate", "w_up", "gate", "up", "dx", "dw_gate", "dw_up", "workspace"),
+                     (x, dh, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace))
+    return _on(device, opt8_gated_ffn_grad(dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(),
+                                           up.data_ptr(), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), workspace.data_ptr(),
+                                           workspace.numel(), rows, d, f, ldx, ldw, lddh, ldg, lddx, lddw, _TYPE[x.dtype],
+                                           act))
 
 
 def opt8_gated_ffn_workspace(rows: int, d: int, f: int) -> int:
@@ -269,21 +280,30 @@ def opt8_gated_ffn_workspace(rows: int, d: int, f: int) -> int:
 
 
 # ----------------------------------------------------------------------------- calls
-def _current_stream():
-    # torch.cuda.current_stream() builds an object for it (3 us, as long as a whole small call)
-    if torch.cuda.is_initialized():
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return _stream_handle(None)
-
-
 def _call(name, desc, stream, check):
-    rc = (_fns or _functions())[name](desc, (_current_stream() if stream is None else _stream_handle(stream)) or None)
+    device = desc.device
+    if device is None:
+        handle = _stream_handle(stream)
+    else:
+        here = torch.cuda.current_device()
+        if here != device:
+            raise ValueError(f"the tensors are on cuda:{device}, but the current device is cuda:{here}")
+        if stream is None:
+            # torch.cuda.current_stream() builds an object for it (3 us, as long as a whole small call)
+            handle = torch._C._cuda_getCurrentRawStream(device)
+        else:
+            where = getattr(stream, "device", None)      # a raw handle does not say
+            if where is not None and where.index != device:
+                raise ValueError(f"the tensors are on cuda:{device}, but the stream is on {where}")
+            handle = _stream_handle(stream)
+    rc = (_fns or _functions())[name](desc, handle or None)
     return _check(rc) if check and rc else rc
 
 
 def opt8_fp8_quantize(quant: opt8_fp8_quant, stream=None, check: bool = True) -> int:
-    """Queue the quantisation on a stream (a torch.cuda.Stream, a raw handle, or None for
-    torch's current stream); the tensors must live until it has run."""
+    """Queue the quantisation on a stream of the tensors' device, which has to be the current
+    one (a torch.cuda.Stream, a raw handle, or None for torch's current stream); the tensors
+    must live until it has run."""
     return _call("opt8_fp8_quantize", quant, stream, check)
 
 

@@ -74,3 +74,21 @@ def test_an_error_that_another_call_left_is_not_the_launch_s():
         assert (rc, message) == (opt8.OPT8_OK, ""), name
         assert found == left, name
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), name
+
+
+def test_a_call_after_the_current_device_changed(monkeypatch):
+    """Descriptors made on cuda:0 are refused while another device is current; nothing is queued."""
+    calls, _keep = every_call()
+    torch.cuda.synchronize()
+    for name, (call, desc, outs) in calls.items():
+        for t in outs:
+            t.fill_(3)
+        with monkeypatch.context() as m:
+            m.setattr(torch.cuda, "current_device", lambda: 1)
+            with pytest.raises(ValueError, match="cuda:0.*current device is cuda:1"):
+                call(desc)
+        torch.cuda.synchronize()
+        assert all(bool((t == 3).all()) for t in outs), name
+        assert call(desc) == opt8.OPT8_OK and call(desc, stream=torch.cuda.current_stream()) == opt8.OPT8_OK
+        torch.cuda.synchronize()
+        assert not all(bool((t == 3).all()) for t in outs), name
