@@ -225,7 +225,7 @@ int gated_backward(const opt8_gated_ffn_grad* a, void* hip_stream) {
       {"dx", dx, a->rows, a->d, a->lddx, 2, true, false},
       {"dw_gate", a->dw_gate, a->f, a->d, a->lddw, 2, true, false},
       {"dw_up", a->dw_up, a->f, a->d, a->lddw, 2, true, false},
-      {"workspace", some ? a->workspace : nullptr, need / 16, 16, 16, 1, true, true},
+      {"workspace", some ? a->workspace : nullptr, need / 16, 1, 1, 16, true, true},    // pieces of 16 bytes
   };
   if ((rc = check_matrices(list, 10))) return rc;
   return launched(launch_gated_ffn_backward(*a, static_cast<hipStream_t>(hip_stream)), "opt8_gated_ffn_backward");

@@ -1,10 +1,12 @@
-"""The operators' binding at the moment of the call, without a GPU: a descriptor belongs to the
-device of its tensors, and so does the stream that it is queued on."""
+"""The operators' calls without a GPU: a descriptor belongs to the device of its tensors, and so
+does the stream that it is queued on; sizes up to the documented limits pass the checks."""
+
+import os
 
 import pytest
 import torch
 
-from precision_optimizer_step_amd import opt8_products as ops
+from precision_optimizer_step_amd import opt8, opt8_products as ops
 
 E4, BF = torch.float8_e4m3fn, torch.bfloat16
 
@@ -57,3 +59,30 @@ def test_a_struct_filled_by_hand_has_no_device(calls):
     _, queued = calls
     assert ops.opt8_fp8_quantize(ops.opt8_fp8_quant(rows=0), stream=9) == 0
     assert queued == [("opt8_fp8_quantize", 9)]
+
+
+@pytest.mark.parametrize("rows,f", [(1 << 17, (1 << 20) - 8), (1 << 22, 1 << 15), ((1 << 22) - 1, 1 << 15), (1 << 18, 1 << 18)])
+def test_the_workspace_of_the_largest_gradients(rows, f):
+    """Matrices of up to 2^37 elements are taken; the workspace, four bytes for each and more,
+    is no matrix and is not held to that count."""
+    if not os.path.exists(opt8.LIB_PATH):
+        pytest.fail("libopt8.so is not built (run __graft_entry__.build())")
+    if torch.cuda.is_available():
+        pytest.skip("the addresses here are made up: checked where no GPU could follow them")
+    names = ["dh", "x", "w_gate", "w_up", "gate", "up", "dx", "dw_gate", "dw_up", "workspace"]
+    apart = 1 << 42
+    at = {n: apart * (i + 1) for i, n in enumerate(names)}
+    need = ops.opt8_gated_ffn_workspace(rows, 8, f)
+    assert rows * f <= 1 << 37 < need < apart
+    kw = dict(rows=rows, d=8, f=f, ldx=8, ldw=8, lddh=f, ldg=f, lddx=8, lddw=8, type=ops.OPT8_TYPE_BF16)
+    rc = ops.opt8_gated_ffn_backward(ops.opt8_gated_ffn_grad(workspace_bytes=need, **at, **kw), stream=0, check=False)
+    assert rc in (opt8.OPT8_OK, opt8.OPT8_E_HIP), opt8.opt8_last_error()      # with no device the launch fails
+    rc = ops.opt8_gated_ffn_backward(ops.opt8_gated_ffn_grad(workspace_bytes=need - 1, **at, **kw), stream=0, check=False)
+    assert rc == opt8.OPT8_E_SIZE
+    # its last bytes are checked against the other buffers like any output's
+    at["x"] = at["workspace"] + need - 16
+    rc = ops.opt8_gated_ffn_backward(ops.opt8_gated_ffn_grad(workspace_bytes=need, **at, **kw), stream=0, check=False)
+    assert rc == opt8.OPT8_E_ALIAS
+    at["x"] += 16
+    rc = ops.opt8_gated_ffn_backward(ops.opt8_gated_ffn_grad(workspace_bytes=need, **at, **kw), stream=0, check=False)
+    assert rc in (opt8.OPT8_OK, opt8.OPT8_E_HIP), opt8.opt8_last_error()
