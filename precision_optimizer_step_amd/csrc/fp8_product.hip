@@ -341,43 +341,21 @@ __global__ __launch_bounds__(256) void product_few_kernel(const Product p) {
 #endif
 }
 
-// The kernel is the one that the estimate calls fastest.  Its constants fit these
-// measurements (us at n = 4096, k = 4096 unless named; TILE, and ROW where it
-// differs; the kernels from left to right):
-//                     256x256    128x128   128x128, 2 teams   64x64, 2 teams   64x64, 4 teams
-//   m =  128             43         21           19                10.8             10.4
-//   m =  512             44         25           21                17.1             23
-//   m = 1024             46         27           25                32               47
-//   m = 2048             50/66      38/43        48                62               90
-//   m = 4096             62/75      74/83        96               119              174
-//   8192 x 8192         244/299    286/327      356               466              670
-//   8192 x 8192, k 512   56         65          107               128              300
-// At most 16 rows go to the kernel without LDS (k = 16384, one row: 12.5 us
-// against 30.5 of the 64x64 tiles; 16 rows: 17.3 against 31.0; but n = 16384, k =
-// 4096, 16 rows: 16.7 against 14.9).
 template <int FA, class C, bool TILE>
 hipError_t launch(Product& p, hipStream_t stream) {
-  if (p.m <= 16) return queue(product_few_kernel<FA, C, TILE>, (p.n + 15) / 16, 256, stream, p);
-  auto tiles = [&](int size) { return static_cast<int64_t>((p.m + size - 1) / size) * ((p.n + size - 1) / size); };
-  const int64_t steps = (p.k + kStepBytes - 1) / kStepBytes;
-  const double cost[5] = {
-      estimate(tiles(256), steps, 256, TILE ? 1.9 : 2.3, 4, TILE ? 1.45 : 1.95, 4),
-      estimate(tiles(128), steps, 512, TILE ? 1.12 : 1.26, 3, 0.78, 3),
-      estimate(tiles(128), steps, 256, 0.70, 3, 0.68, 3),
-      estimate(tiles(64), steps, 512, 0.50, 1.5, 0.32, 1.5),
-      estimate(tiles(64), steps, 256, 0.29, 1.5, 0.28, 1.5),
-  };
-  const int best = static_cast<int>(std::min_element(cost, cost + 5) - cost);
-  const int size = best == 0 ? 256 : best < 3 ? 128 : 64;
+  if (p.m <= kFewRows) return queue(product_few_kernel<FA, C, TILE>, (p.n + 15) / 16, 256, stream, p);
+  const int choice = fp8_choice(p.m, p.n, p.k, TILE), size = tile_size(choice);
   p.tiles_m = (p.m + size - 1) / size;
   p.tiles_n = (p.n + size - 1) / size;
   p.band = std::min(8, p.tiles_m);
-  const unsigned grid = static_cast<unsigned>(tiles(size));
-  if (best == 0) return queue(product_kernel<FA, C, TILE, 256, 256, 2, 4>, grid, 512, stream, p);
-  if (best == 1) return queue(product_kernel<FA, C, TILE, 128, 128, 2, 2>, grid, 256, stream, p);
-  if (best == 2) return queue(product_kernel<FA, C, TILE, 128, 128, 2, 2, 2>, grid, 512, stream, p);
-  if (best == 3) return queue(product_kernel<FA, C, TILE, 64, 64, 2, 1, 2>, grid, 256, stream, p);
-  return queue(product_kernel<FA, C, TILE, 64, 64, 2, 1, 4>, grid, 512, stream, p);
+  const unsigned grid = static_cast<unsigned>(tiles_of(p.m, p.n, size));
+  switch (choice) {
+    case kTile256: return queue(product_kernel<FA, C, TILE, 256, 256, 2, 4>, grid, 512, stream, p);
+    case kTile128: return queue(product_kernel<FA, C, TILE, 128, 128, 2, 2>, grid, 256, stream, p);
+    case kTile128Teams2: return queue(product_kernel<FA, C, TILE, 128, 128, 2, 2, 2>, grid, 512, stream, p);
+    case kTile64Teams2: return queue(product_kernel<FA, C, TILE, 64, 64, 2, 1, 2>, grid, 256, stream, p);
+    default: return queue(product_kernel<FA, C, TILE, 64, 64, 2, 1, 4>, grid, 512, stream, p);
+  }
 }
 
 template <int FA, class C>

@@ -446,42 +446,23 @@ __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dw_kernel(con
 #endif
 }
 
-// Calls f with the tiling that covers `products` results of m x n, k long, in the
-// least time by the estimate.  The constants fit these measurements (us; dx is m x
-// n = rows x d, k = 2f):
-//                                     256     128   128x2 teams  64x2   64x4
-//   dx   500 x 1024, k  8192          151      84        65       48     38
-//   dx  2048 x 1024, k  8192          152      86        68       57     78
-//   dx  2048 x 2560, k 20480          366     251       350      395    531
-//   dx  4096 x 4096, k  8192          195     242       288      414    577
-//   dw  8192 x 1024, k   500           21      15        19       28     45
-//   h    500 x 8192, k  1024           28      14        14       19     30
-//   h   8192 x 32768, k 4096         1641    2134      3074     3956   6194
+// Calls f with the chosen tiling.
 template <class F>
-void with_tiling(int64_t m, int64_t n, int64_t k, int64_t products, F&& f) {
-  auto tiles = [&](int64_t size) { return products * ((m + size - 1) / size) * ((n + size - 1) / size); };
-  const int64_t steps = (k + 63) / 64;
-  const double cost[5] = {
-      estimate(tiles(256), steps, 256, 1.5, 11, 1.3, 11),
-      estimate(tiles(128), steps, 512, 0.97, 7, 0.66, 5),
-      estimate(tiles(128), steps, 256, 0.52, 6, 0.50, 6),
-      estimate(tiles(64), steps, 512, 0.40, 3.5, 0.34, 3),
-      estimate(tiles(64), steps, 256, 0.285, 3.5, 0.28, 3.5),
-  };
-  switch (std::min_element(cost, cost + 5) - cost) {
-    case 0: return f(Tiling<256, 1>{});
-    case 1: return f(Tiling<128, 1>{});
-    case 2: return f(Tiling<128, 2>{});
-    case 3: return f(Tiling<64, 2>{});
+void with_tiling(int choice, F&& f) {
+  switch (choice) {
+    case kTile256: return f(Tiling<256, 1>{});
+    case kTile128: return f(Tiling<128, 1>{});
+    case kTile128Teams2: return f(Tiling<128, 2>{});
+    case kTile64Teams2: return f(Tiling<64, 2>{});
     default: return f(Tiling<64, 4>{});
   }
 }
 
 template <class T>
 hipError_t forward(Forward& p, hipStream_t stream) {
-  if (p.rows <= 16) return queue(gated_forward_few_kernel<T>, (p.f + 15) / 16, 256, stream, p);
+  if (p.rows <= kFewRows) return queue(gated_forward_few_kernel<T>, (p.f + 15) / 16, 256, stream, p);
   hipError_t e = hipSuccess;
-  with_tiling(p.rows, 2 * int64_t{p.f}, p.d, 1, [&](auto g) {
+  with_tiling(gated_forward_choice(p.rows, p.d, p.f), [&](auto g) {
     typedef decltype(g) G;
     p.tiles_m = (p.rows + G::kSize - 1) / G::kSize;
     p.tiles_n = (p.f + G::kSize / 2 - 1) / (G::kSize / 2);
@@ -504,7 +485,7 @@ hipError_t backward(Backward& p, hipStream_t stream) {
     p.tiles_n = static_cast<int>((n + size - 1) / size);
   };
   if (p.dx && p.rows > 0) {
-    with_tiling(p.rows, p.d, 2 * p.width / p.splits, p.splits, [&](auto g) {
+    with_tiling(gated_dx_choice(p.rows, p.d, p.f), [&](auto g) {
       typedef decltype(g) G;
       cover(p.rows, p.d, G::kSize);
       p.band = std::min(8, p.tiles_m);
@@ -517,7 +498,7 @@ hipError_t backward(Backward& p, hipStream_t stream) {
     }
   }
   if (p.dwg) {
-    with_tiling(p.f, p.d, p.rows, 2, [&](auto g) {
+    with_tiling(gated_dw_choice(p.rows, p.d, p.f), [&](auto g) {
       typedef decltype(g) G;
       cover(p.f, p.d, G::kSize);
       p.tiles_m *= 2;

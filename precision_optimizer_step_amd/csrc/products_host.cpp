@@ -18,9 +18,11 @@ int refuse(int code, const char* fmt, ...) {
   return set_last_error(code, text);
 }
 
-// The kernels index rows and columns in 32 bits, a tile's rows by 32-bit byte
-// offsets (256 * 2^23 = 2^31), and launch at most one workgroup for each 2^13
-// results.
+// The kernels index rows and columns in 32 bits and a tile's rows by 32-bit byte
+// offsets (256 * 2^23 = 2^31).  A launch has fewer than 2^32 threads: at 2^37 results
+// the quantiser's has 2^31 (128 x 128 to 256 threads), the products' 2^30 (256 x
+// 256 to 512 or 256 threads: smaller tiles, which would take up to 2^35, are never
+// chosen there), all others stay below 2^29.
 constexpr int64_t kMaxCount = int64_t{1} << 22;
 constexpr int64_t kMaxWidth = int64_t{1} << 20;
 constexpr int64_t kMaxElements = int64_t{1} << 37;
