@@ -29,3 +29,9 @@ GATED = [
     ((1606, 2560, 10240), 0, 1, 0, 1),
     ((4099, 2565, 1001), 0, 0, 1, 1),
 ]
+
+# depths at which each of the four waves of the kernels for few rows runs its loop over four
+# steps of 128 bytes: not at all (and three single steps), once, once and three single steps,
+# several times, and with a last step that is not whole
+FEW_GATED_D = [800, 1024, 1600, 4096, 4100]
+FEW_PRODUCT_K = [1600, 2048, 3400, 4093, 8192]

@@ -95,6 +95,14 @@ def test_gated_backward_in_every_tiling(at, dtype):
         assert untouched(store, got), f"{name}: written outside"
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("rows", [1, 5, 16])
+@pytest.mark.parametrize("d", shapes.FEW_GATED_D)
+def test_gated_forward_of_few_rows_at_depth(rows, d, dtype):
+    for f, act, save in ((100, "silu", True), (77, "gelu", False), (4097, "gelu_tanh", True)):
+        check_forward(rows, d, f, dtype, act, save, rows * 10000 + d)
+
+
 def check_product(m, n, k, kind, block_b, seed):
     g = gen(seed)
     tile = block_b == TILE
@@ -109,6 +117,15 @@ def check_product(m, n, k, kind, block_b, seed):
     worst = dev.worst(c, want, bound, BF)
     assert worst <= 1.0, f"error is {worst} times its bound"
     assert untouched(store, c)
+
+
+@pytest.mark.parametrize("kind", [E4, E5])
+@pytest.mark.parametrize("block_b", [ROW, TILE])
+@pytest.mark.parametrize("m", [1, 7, 16])
+@pytest.mark.parametrize("k", shapes.FEW_PRODUCT_K)
+def test_product_of_few_rows_at_depth(m, k, block_b, kind):
+    for n in (16, 129, 1000):
+        check_product(m, n, k, kind, block_b, m * 10000 + k)
 
 
 @pytest.mark.parametrize("kind", [E4, E5])

@@ -43,6 +43,20 @@ def test_gated_block_reaches_every_tiling(ask):
     assert any(s[4] > 1 for s in shapes.GATED)
 
 
+def test_depths_of_the_kernels_for_few_rows():
+    """By the loops' own arithmetic: a wave takes steps s*w/4 to s*(w+1)/4, four at a time."""
+    for depths, size in ((shapes.FEW_GATED_D, 2), (shapes.FEW_PRODUCT_K, 1)):
+        fours, singles, tails = set(), set(), set()
+        for d in depths:
+            steps = d * size // 128
+            for w in range(4):
+                n = steps * (w + 1) // 4 - steps * w // 4
+                fours.add(n // 4)
+                singles.add(n % 4)
+            tails.add(d * size % 128 != 0)
+        assert {0, 1} <= fours and max(fours) >= 4 and {0, 3} <= singles and tails == {False, True}
+
+
 def test_no_launch_has_too_many_threads(ask):
     """HIP takes fewer than 2^32 threads in a launch: sizes at and beside the powers of two up to
     the documented limits stay below."""
