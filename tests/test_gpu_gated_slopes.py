@@ -77,3 +77,96 @@ def test_no_gradient_stays_none(act):
                                                             torch.full_like(gate, up), None, dwg, dwu, work, act=ACT[act]))
         torch.cuda.synchronize()
         assert bool((dwg == 0).all()) and bool((dwu == 0).all())
+
+
+def value_64(x, wg, wu, act):
+    """h in 64 bits: the activation's value alone, no slope."""
+    return ref.act(x @ wg.t(), act)[0] * (x @ wu.t())
+
+
+def differences(x, wg, wu, c, act, e=1e-4):
+    """Central differences of sum(h * c) by every element of x, w_gate and w_up.  An element of x
+    moves its own row of h alone and one of a weight its own column, so a column of the input is
+    moved at once and h * c summed by rows or by columns."""
+    out = []
+    for at, src in enumerate((x, wg, wu)):
+        grad = torch.empty_like(src)
+        for j in range(src.shape[1]):
+            sums = []
+            for sign in (1, -1):
+                args = [x, wg, wu]
+                args[at] = src.clone()
+                args[at][:, j] += sign * e
+                sums.append((value_64(*args, act) * c).sum(1 if at == 0 else 0))
+            grad[:, j] = (sums[0] - sums[1]) / (2 * e)
+        out.append(grad)
+    return out
+
+
+def difference_bounds(x, wg, wu, c, act):
+    """Bounds of the kernels' gradients against the exact ones of sum(h * c).
+
+    The backward pass reads g and u rounded to bf16 (after fp32 sums): half a step and gamma(d) of
+    the magnitudes.  It takes act and its slope there; |slope| <= 1.13 and |second derivative| <=
+    0.82 (0.5 for silu, 2 phi(0) = 0.798 and a little more for gelu and its tanh form) carry the
+    difference over.  dg and du are rounded once to bf16, then summed in fp32 and rounded once.
+    The slope comes from differences of the value.  The differences themselves are off by e^2/6 of
+    a third derivative (a sum of up to 70 c u act''' x^3, below 300: 5e-7) and by rounding (1e-11)."""
+    half = ref.half_step(BF)
+    g, u = x @ wg.t(), x @ wu.t()
+    n, d = x.shape
+    f = wg.shape[0]
+    v = ref.act(g, act)[0]
+    s = (ref.act(g + 1e-5, act)[0] - ref.act(g - 1e-5, act)[0]) / 2e-5
+    X, G, U, C = (t.abs() for t in (x, wg, wu, c))
+    eg, eu = ((X @ w.t()) * ref.gamma(d) for w in (G, U))
+    eg, eu = eg + half * (g.abs() + eg), eu + half * (u.abs() + eu)
+    slope_err, value_err = 0.82 * eg + 2.0 ** -18, 1.13 * eg + 2.0 ** -18
+    dg, du = (c * u * s).abs(), (c * v).abs()
+    fg = C * (u.abs() * slope_err + eu * (s.abs() + slope_err)) + 2.0 ** -22 * dg
+    fu = C * value_err + 2.0 ** -22 * du
+    fg, fu = fg + half * (dg + fg), fu + half * (du + fu)
+    ag, au = dg + fg, du + fu
+    ex = fg @ G + fu @ U + (ag @ G + au @ U) * ref.gamma(2 * f + 128)
+    ew = [e.t() @ X + (m.t() @ X) * ref.gamma(n) for e, m in ((fg, ag), (fu, au))]
+    return [ref.rounded(t, b, BF) + 1e-6 for t, b in zip(differences(x, wg, wu, c, act), [ex] + ew)]
+
+
+def inputs(rows, d, f, seed):
+    g = torch.Generator().manual_seed(seed)
+    return [(torch.randn(r, k, generator=g) * s).to(BF) for r, k, s in
+            ((rows, d, 1.0), (f, d, d ** -0.5), (f, d, d ** -0.5), (rows, f, 1.0))]
+
+
+@pytest.mark.parametrize("act", list(ACT))
+@pytest.mark.parametrize("rows,d,f", [(40, 48, 56), (9, 72, 33), (70, 17, 24)])
+def test_every_gradient_against_differences(act, rows, d, f):
+    """Element by element.  The bounds are an eighth of the gradients or less (in the 2-norm, over
+    each of the three), so that no gradient, gradients of the other sign, twice the gradient and
+    a slope without its second term all leave them, which is checked here on the 64-bit form."""
+    x, wg, wu, c = inputs(rows, d, f, 3 * rows + d)
+    wide = [t.double() for t in (x, wg, wu, c)]
+    want, bound = differences(*wide, act), difference_bounds(*wide, act)
+    X, G, U, C = wide
+    slope_of_p = ref.act(X @ G.t(), act)[0] / (X @ G.t())           # act(g)/g: the slope without its second term
+    for at, (w, b) in enumerate(zip(want, bound)):
+        assert float(b.norm()) <= float(w.norm()) / 8
+        for wrong in (torch.zeros_like(w), -w, 2 * w):
+            assert float(((wrong - w).abs() / b).max()) > 2.0, at
+    bare = C * (X @ U.t()) * slope_of_p
+    assert float(((bare.t() @ X - want[1]).abs() / bound[1]).max()) > 2.0
+
+    def held(t):
+        store = torch.zeros(t.shape[0], -(-t.shape[1] // 8) * 8, dtype=BF, device="cuda")
+        store[:, :t.shape[1]] = t.cuda()
+        return store[:, :t.shape[1]]
+    xs, gs, us, cs = (held(t) for t in (x, wg, wu, c))
+    h, gate, up = (held(torch.zeros(rows, f)) for _ in range(3))
+    ops.opt8_gated_ffn_forward(ops.make_gated_ffn(xs, gs, us, h, gate, up, act=ACT[act]))
+    outs = [torch.empty(*t.shape, dtype=BF, device="cuda") for t in (x, wg, wu)]
+    work = torch.empty(ops.opt8_gated_ffn_workspace(rows, d, f), dtype=torch.uint8, device="cuda")
+    ops.opt8_gated_ffn_backward(ops.make_gated_ffn_grad(cs, xs, gs, us, gate, up, *outs, work, act=ACT[act]))
+    torch.cuda.synchronize()
+    for name, got, w, b in zip(("dx", "dw_gate", "dw_up"), outs, want, bound):
+        worst = ref.worst(got, w, b)
+        assert worst <= 1.0, f"{name}: error is {worst} times its bound"
