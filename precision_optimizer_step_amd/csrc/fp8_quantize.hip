@@ -101,8 +101,9 @@ __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
 // both orientations.  A row's maximum is reduced over its 16 lanes, a column's
 // over the 16 row groups through LDS.  The transposed codes leave as 8-byte
 // runs of a column, four lanes of a wave side by side.  Bound by memory: 16384 x
-// 4096 bf16 by tiles, both ways, 61 us (4.4 TB/s); 4001 x 10240 by rows, both ways,
-// 42 us (4.0 TB/s).
+// 4096 bf16 by tiles, both ways, 62 us (4.3 TB/s); 4001 x 10240 by rows, both ways,
+// 44 us (3.8 TB/s); 48 and 33 us where the last call's data, the same, are still in the
+// last-level cache.
 template <class X, int F, bool TILE, bool Q, bool T>
 __global__ __launch_bounds__(256) void quantize_kernel(const Quant p) {
   __shared__ float tops[16][128];

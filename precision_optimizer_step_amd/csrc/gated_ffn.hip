@@ -14,8 +14,10 @@ namespace {
 using namespace tile;
 
 // ------------------------------------------------------------- activations
-// exp by the hardware's base-2 exponential of x*log2(e): about 2^-22 relative,
-// far below a 16-bit result's half step.  sigmoid(-inf) = 0 and sigmoid(inf) = 1.
+// exp by the hardware's base-2 exponential (2^-23.5 relative) of x*log2(e), whose
+// rounding to fp32 adds |x| 2^-24: measured 2^-23 for |x| < 1, 2^-21 to 8, 2^-19 to 24
+// and 2^-18 at the end of the range, far below a 16-bit result's half step.
+// sigmoid(-inf) = 0 and sigmoid(inf) = 1.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x)); }
 
@@ -90,7 +92,8 @@ struct Forward {
 // A tile holds B/2 rows of Wg and the same rows of Wu beside B rows of x; a
 // wave takes as many columns of one as of the other, so g and u of one h meet
 // in one lane.  8192 rows, d 4096, f 16384: 1.54 ms, with both projections stored
-// 1.66 (1.33 PFLOP/s); about 10 us of a tile's 100 are its epilogue.
+// 1.66 (1.33 PFLOP/s); about 10 us of a tile's 100 are its epilogue.  (The 256 x 256
+// bf16 kernel spills 4 registers, outside the step loop.)
 template <class T, class G>
 __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_forward_kernel(const Forward p) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -287,7 +290,7 @@ __device__ __forceinline__ float slope_product(float dh, float slope, float up) 
 }
 
 // dg and du, rounded to the type that the products take, zeros in the columns
-// from f to width; 8 columns a thread.  8192 x 16384: 210 us, 1.34 GB at 6.4 TB/s.
+// from f to width; 8 columns a thread.  8192 x 16384: 215 us, 1.34 GB at 6.2 TB/s.
 template <class T>
 __global__ __launch_bounds__(256) void gated_slopes_kernel(const Backward p) {
   const int64_t per = p.width / 8;
@@ -361,7 +364,8 @@ __device__ __forceinline__ void store_tile(char* copies, Out* out, int64_t ld, i
     }
 }
 
-// dx = [dg du] [Wg; Wu]: k runs along the rows of the weights.
+// dx = [dg du] [Wg; Wu]: k runs along the rows of the weights.  (The 256 x 256 kernel
+// spills 20 registers, outside the step loop.)
 template <class T, class G>
 __global__ __launch_bounds__(G::kThreads, G::kMinWaves) void gated_dx_kernel(const Backward p) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -7,10 +7,13 @@
 // direct global-to-LDS loads fill the other, so a tile's latency has most of a
 // step to pass and no register holds it on the way.
 //
-// Operand tiles in LDS, both swizzled so that neither the loads' linear
-// writes nor the fragment reads meet bank conflicts (16-byte chunks; the loads
-// write LDS in lane order, so it is the lane's global address that is permuted);
-// counted: none for rows, 1 to 2 cycles an access for the transposing reads):
+// Operand tiles in LDS, both swizzled against bank conflicts between the loads'
+// linear writes and the fragment reads (16-byte chunks; the loads write LDS in
+// lane order, so it is the lane's global address that is permuted).  Counted: none
+// for rows; for the transposing reads 1 to 2 cycles an access in tiles of 128 and
+// 256 columns, 4.3 in tiles of 64, whose rows of 8 chunks leave the swizzle one bit of
+// the row's number, the one that already chooses the half of a 256-byte line of
+// banks (twice the passes of the wider tiles, counting addresses):
 //  - rows: [tile row][8 chunks of k], chunk c at slot c ^ key(row);
 //  - cols (16-bit, an operand whose k runs along the rows of its matrix):
 //    [64 k][tile columns], chunk c at slot c ^ (key(k) << 2), read with the
