@@ -47,7 +47,7 @@ struct Product {
 // use accumulation registers: hence 128 x 64 results to a wave and two waves a
 // SIMD.  8192 x 16384 x 4096, TILE: 479 us, 2.29 PFLOP/s, matrix core 61% busy at
 // 1.8 GHz, a third of the waves' cycles at the barrier.  (The 256 x 256 kernel with ROW
-// scales spills 4 registers, outside the step loop.)
+// scales spills 4 registers, read again in a ragged last step and behind the loop alone.)
 //
 // KG > 1: KG teams of WM x WN waves share the tile's steps in turn, each with its
 // own copies, and add their sums through LDS at the end, in a fixed order: for
