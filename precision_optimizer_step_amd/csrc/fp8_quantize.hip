@@ -1,10 +1,9 @@
 // 8-bit codes and block scales of a matrix, of its transpose, or of both from
 // one read of it.
 #include <algorithm>
-#include <type_traits>
 
+#include "fp8_codes.h"
 #include "products_internal.h"
-#include "tile_product.h"
 
 namespace opt8 {
 namespace {
@@ -20,81 +19,6 @@ struct Quant {
   int64_t rows, cols, ldx, ldq, ldt;
   int cb, rb;    // blocks of columns and of rows
 };
-
-template <class X> struct Raw { typedef uint16_t type; };
-template <> struct Raw<float> { typedef float type; };
-
-// 8 consecutive values as they lie in memory (16-bit ones stay packed until they
-// are used: 32 registers for a thread's 64 values instead of 64); `left` of them
-// exist, the others are zero.
-template <class X>
-struct Eight {
-  i16x8 v;
-  __device__ __forceinline__ void zero() { v = i16x8{0, 0, 0, 0, 0, 0, 0, 0}; }
-  __device__ __forceinline__ void load(const uint16_t* p, int64_t left) {
-    if (left >= 8) {
-      v = __builtin_bit_cast(i16x8, static_cast<i32x4>(*reinterpret_cast<const i32x4_at2*>(p)));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < left ? static_cast<short>(p[i]) : 0;
-    }
-  }
-  __device__ __forceinline__ float operator[](int i) const { return value_of<X>(static_cast<uint16_t>(v[i])); }
-};
-template <>
-struct Eight<float> {
-  float v[8];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  }
-  __device__ __forceinline__ void load(const float* p, int64_t left) {
-    if (left >= 8) {
-      const f32x4 a = *reinterpret_cast<const f32x4_at4*>(p), b = *reinterpret_cast<const f32x4_at4*>(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
-    }
-  }
-  __device__ __forceinline__ float operator[](int i) const { return v[i]; }
-};
-
-// The largest of the 16 lanes of a row, in every one of them: rotations by 1, 2,
-// 4 and 8 lanes.
-template <int CONTROL>
-__device__ __forceinline__ float rotated(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CONTROL, 0xf, 0xf, false));
-}
-__device__ __forceinline__ float largest_of_16(float x) {
-  x = __builtin_fmaxf(x, rotated<0x121>(x));
-  x = __builtin_fmaxf(x, rotated<0x122>(x));
-  x = __builtin_fmaxf(x, rotated<0x124>(x));
-  return __builtin_fmaxf(x, rotated<0x128>(x));
-}
-
-// The largest magnitude so far; NaN does not count (fmaxf returns the other).
-__device__ __forceinline__ float larger(float top, float x) { return __builtin_fmaxf(top, __builtin_fabsf(x)); }
-
-template <int F> constexpr float kLargest = F == 0 ? 448.0f : 57344.0f;
-template <int F>
-__device__ __forceinline__ float scale_of(float top) { return __builtin_fmaxf(top / kLargest<F>, 0x1p-126f); }
-
-// Codes of four values.  No product passes the largest value by more than its
-// own rounding, so the conversion cannot overflow.
-template <int F>
-__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
-  int w = 0;
-  if constexpr (F == 0) {
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-  } else {
-    w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, w, false);
-    w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
-  }
-  return static_cast<uint32_t>(w);
-}
 
 // A workgroup takes one 128 x 128 tile: thread t holds the 8 x 8 values of
 // rows 8*(t/16).. and columns 8*(t%16).. in registers, so x is read once for

@@ -1,0 +1,58 @@
+// 8 consecutive values of a row: loads, sums in 32 bits and stores, for the
+// kernels whose lanes take a row in pieces of 8.
+#pragma once
+
+#include "tile_product.h"
+
+namespace opt8 {
+namespace tile {
+
+template <class X> struct Raw { typedef uint16_t type; };
+template <> struct Raw<float> { typedef float type; };
+
+// 8 consecutive values as they lie in memory (16-bit ones stay packed until they
+// are used: 32 registers for a thread's 64 values instead of 64); `left` of them
+// exist, the others are zero.
+template <class X>
+struct Eight {
+  i16x8 v;
+  __device__ __forceinline__ void zero() { v = i16x8{0, 0, 0, 0, 0, 0, 0, 0}; }
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t left) {
+    if (left >= 8) {
+      v = __builtin_bit_cast(i16x8, static_cast<i32x4>(*reinterpret_cast<const i32x4_at2*>(p)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < left ? static_cast<short>(p[i]) : 0;
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const { return value_of<X>(static_cast<uint16_t>(v[i])); }
+};
+template <>
+struct Eight<float> {
+  float v[8];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  }
+  __device__ __forceinline__ void load(const float* p, int64_t left) {
+    if (left >= 8) {
+      const f32x4 a = *reinterpret_cast<const f32x4_at4*>(p), b = *reinterpret_cast<const f32x4_at4*>(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const { return v[i]; }
+};
+
+// The first `left` (at most 8) of 8 values, each rounded once to X.
+template <class X>
+__device__ __forceinline__ void store_eight(typename Raw<X>::type* p, const float* v, int64_t left) {
+  if constexpr (sizeof(typename Raw<X>::type) == 4) store_some(p, v, left);
+  else store_some(p, packed<X>(v), left);
+}
+
+}  // namespace tile
+}  // namespace opt8

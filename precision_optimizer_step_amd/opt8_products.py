@@ -280,22 +280,25 @@ def opt8_gated_ffn_workspace(rows: int, d: int, f: int) -> int:
 
 
 # ----------------------------------------------------------------------------- calls
-def _call(name, desc, stream, check):
+def _queue_on(desc, stream):
+    """The handle of the stream that a descriptor is to be queued on."""
     device = desc.device
     if device is None:
-        handle = _stream_handle(stream)
-    else:
-        here = torch.cuda.current_device()
-        if here != device:
-            raise ValueError(f"the tensors are on cuda:{device}, but the current device is cuda:{here}")
-        if stream is None:
-            # torch.cuda.current_stream() builds an object for it (3 us, as long as a whole small call)
-            handle = torch._C._cuda_getCurrentRawStream(device)
-        else:
-            where = getattr(stream, "device", None)      # a raw handle does not say
-            if where is not None and where.index != device:
-                raise ValueError(f"the tensors are on cuda:{device}, but the stream is on {where}")
-            handle = _stream_handle(stream)
+        return _stream_handle(stream)
+    here = torch.cuda.current_device()
+    if here != device:
+        raise ValueError(f"the tensors are on cuda:{device}, but the current device is cuda:{here}")
+    if stream is None:
+        # torch.cuda.current_stream() builds an object for it (3 us, as long as a whole small call)
+        return torch._C._cuda_getCurrentRawStream(device)
+    where = getattr(stream, "device", None)      # a raw handle does not say
+    if where is not None and where.index != device:
+        raise ValueError(f"the tensors are on cuda:{device}, but the stream is on {where}")
+    return _stream_handle(stream)
+
+
+def _call(name, desc, stream, check):
+    handle = _queue_on(desc, stream)
     rc = (_fns or _functions())[name](desc, handle or None)
     return _check(rc) if check and rc else rc
 
