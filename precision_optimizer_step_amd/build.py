@@ -12,7 +12,9 @@ LIB = os.path.join(HERE, "libopt8.so")
 SOURCES = [os.path.join(HERE, "csrc", "opt8_host.cpp"), os.path.join(HERE, "csrc", "opt8_tables.cpp"),
            os.path.join(HERE, "csrc", "opt8_kernels.hip"), os.path.join(HERE, "csrc", "opt8_map.hip"),
            os.path.join(HERE, "csrc", "products_host.cpp"), os.path.join(HERE, "csrc", "fp8_quantize.hip"),
-           os.path.join(HERE, "csrc", "fp8_product.hip"), os.path.join(HERE, "csrc", "gated_ffn.hip")]
+           os.path.join(HERE, "csrc", "fp8_product.hip"), os.path.join(HERE, "csrc", "gated_ffn.hip"),
+           os.path.join(HERE, "csrc", "layers_host.cpp"), os.path.join(HERE, "csrc", "embedding.hip"),
+           os.path.join(HERE, "csrc", "rms_norm.hip"), os.path.join(HERE, "csrc", "grad_norm.hip")]
 # bandwidth probe used by bench.py for the attainable-bandwidth context figure
 PROBE_LIB = os.path.join(HERE, "libopt8_probe.so")
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "bw_probe.hip")]

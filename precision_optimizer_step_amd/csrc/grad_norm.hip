@@ -1,0 +1,164 @@
+// Norm of a list of gradients, and their clipping.
+#include <algorithm>
+
+#include "layers_internal.h"
+#include "vectors.h"
+
+namespace opt8 {
+namespace {
+
+using namespace tile;
+
+constexpr int kThreads = 256;
+constexpr int kPasses = OPT8_GRAD_PIECE / (kThreads * 8);    // 8 values to a thread in each
+
+struct NormOf {
+  const GradPiece* table;
+  int64_t pieces;
+  double* sums;       // [groups]
+  double* squares;
+  float* norm;
+  int groups;
+};
+
+// Sum over a workgroup, in its first thread.
+__device__ __forceinline__ double sum_of_group(double x) {
+  __shared__ double waves[kThreads / 64];
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) x += __shfl_xor(x, s);
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = waves[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 64; ++w) x += waves[w];
+  return x;
+}
+
+// Squares in 64 bits: exact, and no gradient's is too large or too small for them.
+template <class X>
+__device__ __forceinline__ void add_squares(const GradPiece& p, double* sum) {
+  const auto* from = static_cast<const typename Raw<X>::type*>(p.from);
+  Eight<X> v[kPasses];
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) {
+    const int at = (k * kThreads + static_cast<int>(threadIdx.x)) * 8;
+    v[k].zero();
+    if (at < p.count) v[k].load(from + at, p.count - at);
+  }
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double x = static_cast<double>(v[k][i]);
+      sum[i & 1] = __builtin_fma(x, x, sum[i & 1]);
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void squares_kernel(const NormOf p) {
+  double sum[2] = {0.0, 0.0};
+  for (int64_t i = blockIdx.x; i < p.pieces; i += p.groups) {
+    const GradPiece piece = p.table[i];
+    if (piece.type == OPT8_TYPE_BF16) add_squares<Bf16>(piece, sum);
+    else if (piece.type == OPT8_TYPE_FP16) add_squares<Fp16>(piece, sum);
+    else add_squares<float>(piece, sum);
+  }
+  const double all = sum_of_group(sum[0] + sum[1]);
+  if (threadIdx.x == 0) p.sums[blockIdx.x] = all;
+}
+
+// The workgroups' sums, by one more.
+__global__ __launch_bounds__(kThreads) void norm_kernel(const NormOf p) {
+  double sum = 0.0;
+#pragma unroll
+  for (int k = 0; k < kGradGroups / kThreads; ++k) {
+    const int i = k * kThreads + static_cast<int>(threadIdx.x);
+    if (i < p.groups) sum += p.sums[i];
+  }
+  sum = sum_of_group(sum);
+  if (threadIdx.x != 0) return;
+  *p.squares = sum;
+  if (p.norm) *p.norm = static_cast<float>(__builtin_sqrt(sum));
+}
+
+struct Clip {
+  const GradPiece* table;
+  int64_t pieces;
+  const double* squares;
+  float* norm;
+  double max_norm;
+  int groups;
+};
+
+template <class X, class Y>
+__device__ __forceinline__ void scaled(const GradPiece& p, float factor) {
+  const auto* from = static_cast<const typename Raw<X>::type*>(p.from);
+  auto* to = static_cast<typename Raw<Y>::type*>(p.to);
+  Eight<X> v[kPasses];
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) {
+    const int at = (k * kThreads + static_cast<int>(threadIdx.x)) * 8;
+    v[k].zero();
+    if (at < p.count) v[k].load(from + at, p.count - at);
+  }
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) {
+    const int at = (k * kThreads + static_cast<int>(threadIdx.x)) * 8;
+    float out[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = v[k][i] * factor;
+    if (at < p.count) store_eight<Y>(to + at, out, p.count - at);
+  }
+}
+
+template <class X>
+__device__ __forceinline__ void scaled_to(const GradPiece& p, float factor) {
+  if (p.to_type == OPT8_TYPE_BF16) scaled<X, Bf16>(p, factor);
+  else if (p.to_type == OPT8_TYPE_FP16) scaled<X, Fp16>(p, factor);
+  else scaled<X, float>(p, factor);
+}
+
+__global__ __launch_bounds__(kThreads) void clip_kernel(const Clip p) {
+  const double norm = __builtin_sqrt(*p.squares);
+  if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = static_cast<float>(norm);
+  const double ratio = p.max_norm / (norm + 1e-6);
+  const float factor = ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);    // NaN stays NaN
+  for (int64_t i = blockIdx.x; i < p.pieces; i += p.groups) {
+    const GradPiece piece = p.table[i];
+    if (factor == 1.0f && piece.from == piece.to) continue;
+    if (piece.type == OPT8_TYPE_BF16) scaled_to<Bf16>(piece, factor);
+    else if (piece.type == OPT8_TYPE_FP16) scaled_to<Fp16>(piece, factor);
+    else scaled_to<float>(piece, factor);
+  }
+}
+
+int groups_of(int64_t pieces) { return static_cast<int>(std::min<int64_t>(pieces, kGradGroups)); }
+
+}  // namespace
+
+hipError_t launch_grad_norm(const opt8_grads& a, hipStream_t stream) {
+  NormOf p;
+  p.table = static_cast<const GradPiece*>(a.table);
+  p.pieces = a.pieces;
+  p.sums = static_cast<double*>(a.workspace);
+  p.squares = a.squares;
+  p.norm = a.norm;
+  p.groups = groups_of(a.pieces);
+  if (p.groups > 0) {
+    const hipError_t e = queue(squares_kernel, static_cast<unsigned>(p.groups), kThreads, stream, p);
+    if (e != hipSuccess) return e;
+  }
+  return queue(norm_kernel, 1, kThreads, stream, p);
+}
+
+hipError_t launch_grad_clip(const opt8_grads& a, hipStream_t stream) {
+  Clip p;
+  p.table = static_cast<const GradPiece*>(a.table);
+  p.pieces = a.pieces;
+  p.squares = a.squares;
+  p.norm = a.norm;
+  p.max_norm = a.max_norm;
+  p.groups = std::max(1, groups_of(a.pieces));
+  return queue(clip_kernel, static_cast<unsigned>(p.groups), kThreads, stream, p);
+}
+
+}  // namespace opt8

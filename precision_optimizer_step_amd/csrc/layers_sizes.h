@@ -1,0 +1,73 @@
+// How the operators in opt8_layers.h cut their work and their workspaces: pure
+// functions of the sizes, without HIP, so that a host program can ask them too.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+namespace opt8 {
+
+inline int64_t pieces_of(int64_t n, int64_t each) { return (n + each - 1) / each; }
+inline int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// ---------------------------------------------------------------- embedding's gradient
+// Ids of the table to a workgroup of the sort, which counts them in LDS.
+constexpr int kSortWaves = 8;
+constexpr int kSortRange = 1024;
+inline int64_t sort_range(int64_t vocab) {
+  return std::min<int64_t>(kSortRange, std::max<int64_t>(1, pieces_of(vocab, 256)));
+}
+
+// Sorted tokens that a wave adds up: 32 where that leaves at least 4096 waves (4 to a
+// SIMD), fewer for short batches; at most 32 (a wave keeps a chunk's tokens and its two
+// neighbours in its lanes).
+inline int64_t sum_chunk(int64_t tokens, int64_t d) {
+  const int64_t waves = tokens * pieces_of(d, 512);
+  return waves >= 32 * 4096 ? 32 : waves >= 16 * 4096 ? 16 : 8;
+}
+
+struct EmbeddingSpace {
+  int64_t order, keys, starts, partial, bytes;    // offsets
+};
+inline EmbeddingSpace embedding_space(int64_t tokens, int64_t vocab, int64_t d) {
+  EmbeddingSpace s;
+  s.order = 0;
+  s.keys = align16(4 * tokens);
+  s.starts = s.keys + align16(4 * tokens);
+  s.partial = s.starts + align16(4 * (vocab + 1));
+  // two sums of each chunk: of the id that it shares with the one before, and with the one behind
+  s.bytes = s.partial + align16(8 * d * pieces_of(tokens, sum_chunk(tokens, d)));
+  return s;
+}
+
+// ---------------------------------------------------------------- norm's backward pass
+// Lanes that share a row, and pieces of 8 values that each of them holds.
+struct RowShape {
+  int lanes, pieces;
+};
+constexpr int64_t kNormHeld = 16384;    // longer rows are read twice
+inline RowShape norm_grad_shape(int64_t d) {
+  if (d <= 128) return {16, 1};
+  if (d <= 512) return {64, 1};
+  if (d <= 1024) return {64, 2};
+  if (d <= 2048) return {256, 1};
+  if (d <= 4096) return {256, 2};
+  if (d <= 8192) return {1024, 1};
+  return {1024, 2};
+}
+// Workgroups that each keep a sum of dweight, and so rows of the workspace.
+inline int64_t norm_grad_groups(int64_t rows, int64_t d) {
+  if (d > kNormHeld) return std::max<int64_t>(1, std::min<int64_t>(64, rows / 8));
+  const int64_t lanes = norm_grad_shape(d).lanes;
+  const int64_t at_once = lanes <= 256 ? 256 / lanes : 1;      // rows to a workgroup at a time
+  const int64_t most = lanes <= 256 ? 1024 : 512;
+  return std::max<int64_t>(1, std::min<int64_t>(most, pieces_of(rows, at_once)));
+}
+inline int64_t norm_grad_space(int64_t rows, int64_t d) {
+  return rows <= 0 ? 0 : align16(4 * d * norm_grad_groups(rows, d));
+}
+
+// ---------------------------------------------------------------- gradients' norm
+constexpr int64_t kGradGroups = 2048;    // workgroups that each keep a sum: 8 to a CU
+
+}  // namespace opt8
