@@ -19,7 +19,7 @@
  * their element's own alignment only and are faster on 16 bytes (8-bit codes:
  * 16-byte rows, as in opt8_products.h).  What lies behind a row's end is neither
  * read nor written.  No count of rows exceeds 2^22, none of columns 2^20, no matrix
- * 2^37 elements, no ld 2^38.  An output may not overlap another buffer of the call,
+ * 2^34 elements, no ld 2^38.  An output may not overlap another buffer of the call,
  * except where a call says that it may be the same one.
  *
  * Status codes of these calls: OPT8_E_NULL (a required pointer), OPT8_E_SIZE
@@ -155,7 +155,8 @@ typedef struct opt8_grad {
   int32_t out_type;          /* likewise; read where out is not NULL                 */
 } opt8_grad;
 
-/* The list as the kernels read it: pieces of at most 8192 values, 24 bytes each.
+/* The list as the kernels read it: 24 bytes, and 24 for each piece of at most 8192
+ * values of a gradient.
  * opt8_grad_table_bytes gives its size (or a negative status) and opt8_grad_table
  * writes it to HOST memory; the caller copies it to the device, and passes that copy
  * as often as it likes while the gradients stay at their addresses.  No two buffers
@@ -170,7 +171,7 @@ int opt8_grad_table(const opt8_grad* grads, int32_t n, void* host_table, int64_t
 
 typedef struct opt8_grads {
   const void* table;         /* device copy of a list's table, 8-byte aligned         */
-  int64_t pieces;            /* its bytes / OPT8_GRAD_PIECE_BYTES; >= 0              */
+  int64_t table_bytes;       /* what opt8_grad_table_bytes gave for the list         */
   double* squares;           /* [1]                                                  */
   float* norm;               /* [1], or NULL                                         */
   void* workspace;           /* 16-byte aligned                                      */

@@ -27,72 +27,80 @@ struct Lookup {
   int column_blocks;
 };
 
-// A wave takes 512 columns of kTokens tokens, 8 columns to a lane; its rows are
-// loaded before the first is stored.
-constexpr int kTokens = 4;
+// A wave takes 512 columns of kTokens tokens, 8 columns to a lane.  One load brings the
+// tokens' ids and one their places (a lane each), the next ones all rows.
+constexpr int kTokens = 2;
 template <class X, class Id>
 __global__ __launch_bounds__(256) void lookup_kernel(const Lookup p) {
   const int64_t task = int64_t{blockIdx.x} * 4 + wave_id();
   if (task >= p.tasks) return;
+  const int lane = threadIdx.x & 63;
   const int64_t first = task / p.column_blocks * kTokens;
-  const int64_t c = task % p.column_blocks * 512 + (threadIdx.x & 63) * 8;
+  const int64_t c = task % p.column_blocks * 512 + lane * 8;
   const int64_t left = p.d - c;
-  if (left <= 0) return;
   typedef typename Raw<X>::type Value;
+  const bool some = lane < kTokens && first + lane < p.tokens;
+  const int ids = some ? row_of<Id>(p.ids, first + lane, p.vocab) : -1;
+  const int places = some && p.place_ids ? row_of<Id>(p.place_ids, first + lane, p.places) : -1;
   Eight<X> v[kTokens], at[kTokens];
 #pragma unroll
   for (int t = 0; t < kTokens; ++t) {
     v[t].zero();
     at[t].zero();
-    if (first + t >= p.tokens) continue;
-    const int id = row_of<Id>(p.ids, first + t, p.vocab);
-    if (id >= 0) v[t].load(static_cast<const Value*>(p.table) + id * p.ldtable + c, left);
-    if (p.place_ids) {
-      const int place = row_of<Id>(p.place_ids, first + t, p.places);
-      if (place >= 0) at[t].load(static_cast<const Value*>(p.place_table) + place * p.ldplace + c, left);
-    }
+    const int64_t id = __builtin_amdgcn_readlane(ids, t), place = __builtin_amdgcn_readlane(places, t);
+    if (id >= 0 && left > 0) v[t].load(static_cast<const Value*>(p.table) + id * p.ldtable + c, left);
+    if (place >= 0 && left > 0) at[t].load(static_cast<const Value*>(p.place_table) + place * p.ldplace + c, left);
   }
 #pragma unroll
   for (int t = 0; t < kTokens; ++t) {
-    if (first + t >= p.tokens) continue;
+    if (first + t >= p.tokens || left <= 0) break;
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       y[i] = v[t][i] * p.scale;
       if (p.place_ids) y[i] += at[t][i];
     }
-    store_eight<X>(static_cast<Value*>(p.y) + (first + t) * p.ldy + c, y, left);
+    stream_eight<X>(static_cast<Value*>(p.y) + (first + t) * p.ldy + c, y, left);
   }
 }
 
 // ---------------------------------------------------------------- gradient
-// The tokens sorted by id, those of one id by their place: a workgroup owns a range of
-// ids and reads all of them twice, once to count and once to place.  Waves read
-// consecutive stretches, and each has its own counter for every id, so that
-// a token's position depends on the ids alone.
+// Where an id's tokens start among the sorted ones stands in starts[slot_of(id)], and
+// where they end in the next place: id / groups within the workgroup's ids.
+__device__ __forceinline__ int slot_of(int id, const SortShape& s) { return (id & (s.groups - 1)) * s.range + (id >> s.shift); }
+
+// The tokens sorted by their id's slot, those of one id by their place: a workgroup
+// owns a share of the ids and reads all tokens, counting its own ones and noting where
+// they stand, and then gives them their positions.  Waves read consecutive stretches,
+// and each has its own counter for every id, so that a token's position depends on the
+// ids alone.  A wave that finds more than it can note (an id with a sixteenth of over
+// 2^13 tokens) reads its stretch again.
 struct Sort {
   const void* ids;
   int64_t tokens, vocab;
-  int range;
+  SortShape shape;
   int* order;     // token numbers
   int* keys;      // their ids
-  int* starts;    // [vocab + 1], of each id's first
+  int* starts;    // [groups * range + 1]
 };
 
 template <class Id>
 __global__ __launch_bounds__(64 * kSortWaves) void sort_kernel(const Sort p) {
-  constexpr int kThreads = 64 * kSortWaves, kUnroll = 8;
-  __shared__ int count[kSortRange * kSortWaves];    // [id of the range][wave]
+  constexpr int kThreads = 64 * kSortWaves, kUnroll = 8, kNoted = 512;
+  __shared__ int count[kSortRange * kSortWaves];    // [id of the workgroup][wave]
+  __shared__ int noted[kSortWaves][kNoted];         // id of the workgroup << kPlaceBits | place in the wave's stretch
   __shared__ int sums[kSortWaves], belows[kSortWaves];
+  constexpr int kPlaceBits = 19;
+  static_assert(kSortRange <= 1 << (31 - kPlaceBits) && (1 << 22) / kSortWaves + 64 <= 1 << kPlaceBits, "a note's bits");
   const int t = threadIdx.x, lane = t & 63, wave = wave_id();
-  const int low = static_cast<int>(blockIdx.x) * p.range;
-  const int range = min(p.range, static_cast<int>(p.vocab) - low);
+  const int group = static_cast<int>(blockIdx.x), mask = p.shape.groups - 1, shift = p.shape.shift, range = p.shape.range;
   for (int i = t; i < range * kSortWaves; i += kThreads) count[i] = 0;
   __syncthreads();
 
-  const int64_t each = (p.tokens + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64;
+  const int64_t each = (p.tokens + kThreads - 1) / kThreads * 64;
   const int64_t begin = wave * each, end = begin + each < p.tokens ? begin + each : p.tokens;
-  int below = 0;
+  const uint64_t under = (uint64_t{1} << lane) - 1;
+  int below = 0, found = 0;
   for (int64_t i0 = begin; i0 < end; i0 += 64 * kUnroll) {
     int id[kUnroll];
 #pragma unroll
@@ -102,8 +110,16 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_kernel(const Sort p) {
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (id[u] >= 0 && id[u] < low) ++below;
-      if (id[u] >= low && id[u] < low + range) atomicAdd(&count[(id[u] - low) * kSortWaves + wave], 1);
+      const int owner = id[u] < 0 ? p.shape.groups : id[u] & mask;
+      below += owner < group;
+      const uint64_t mine = __ballot(owner == group);
+      if (mine == 0) continue;
+      if (owner == group) {
+        const int own = id[u] >> shift, at = found + __builtin_popcountll(mine & under);
+        atomicAdd(&count[own * kSortWaves + wave], 1);
+        if (at < kNoted) noted[wave][at] = own << kPlaceBits | static_cast<int>(i0 - begin + 64 * u + lane);
+      }
+      found += __builtin_popcountll(mine);
     }
   }
 #pragma unroll
@@ -134,37 +150,41 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_kernel(const Sort p) {
   for (int i = from; i < to; ++i) {
     const int n = count[i];
     count[i] = at;
-    if (i % kSortWaves == 0) p.starts[low + i / kSortWaves] = at;
+    if (i % kSortWaves == 0) p.starts[group * range + i / kSortWaves] = at;
     at += n;
   }
-  if (t == 0 && low + range == p.vocab) p.starts[p.vocab] = total;
+  if (t == 0 && group == mask) p.starts[p.shape.groups * range] = total;
   __syncthreads();
 
-  for (int64_t i0 = begin; i0 < end; i0 += 64 * kUnroll) {
-    int id[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = i0 + 64 * u + lane;
-      id[u] = i < end ? row_of<Id>(p.ids, i, p.vocab) : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      uint64_t open = __ballot(id[u] >= low && id[u] < low + range);
-      while (open) {      // the ids among these 64, each once
-        const int one = __builtin_amdgcn_readlane(id[u], __builtin_ctzll(open));
-        const uint64_t same = __ballot(id[u] == one);
-        int* next = &count[(one - low) * kSortWaves + wave];
-        const int first = *next;
-        if (id[u] == one) {
-          const int to_ = first + __builtin_popcountll(same & ((uint64_t{1} << lane) - 1));
-          p.order[to_] = static_cast<int>(i0 + 64 * u + lane);
-          p.keys[to_] = one;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (lane == 0) *next = first + __builtin_popcountll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        open &= ~same;
+  // Positions for 64 tokens of the wave's, in their order: own < 0 where there is none.
+  auto place = [&](int own, int64_t token) {
+    uint64_t open = __ballot(own >= 0);
+    while (open) {      // the ids among them, each once
+      const int one = __builtin_amdgcn_readlane(own, __builtin_ctzll(open));
+      const uint64_t same = __ballot(own == one);
+      int* next = &count[one * kSortWaves + wave];
+      const int first = *next;
+      if (own == one) {
+        const int to = first + __builtin_popcountll(same & under);
+        p.order[to] = static_cast<int>(token);
+        p.keys[to] = one << shift | group;
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (lane == 0) *next = first + __builtin_popcountll(same);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      open &= ~same;
+    }
+  };
+  if (found <= kNoted) {
+    for (int i = lane; i - lane < found; i += 64) {
+      const int note = i < found ? noted[wave][i] : -1;
+      place(note < 0 ? -1 : note >> kPlaceBits, begin + (note & ((1 << kPlaceBits) - 1)));
+    }
+  } else {
+    for (int64_t i0 = begin; i0 < end; i0 += 64) {
+      const int64_t i = i0 + lane;
+      const int id = i < end ? row_of<Id>(p.ids, i, p.vocab) : -1;
+      place(id >= 0 && (id & mask) == group ? id >> shift : -1, i);
     }
   }
 }
@@ -173,6 +193,7 @@ struct Sum {
   const int* order;
   const int* keys;
   const int* starts;
+  SortShape shape;
   const void* dy;
   void* dtable;
   float* partial;    // [chunk][2][d]
@@ -198,6 +219,14 @@ __device__ __forceinline__ void finish(const Sum& p, int id, int64_t c, int64_t 
   store_eight<D>(out, sum, left);
 }
 
+// Zeros in 512 columns of one row, by a wave.
+template <class D>
+__device__ __forceinline__ void clear(void* dtable, int64_t row, int64_t block, int64_t d, int64_t ld) {
+  const float none[8] = {};
+  const int64_t c = block * 512 + (threadIdx.x & 63) * 8;
+  if (c < d) stream_eight<D>(static_cast<typename Raw<D>::type*>(dtable) + row * ld + c, none, d - c);
+}
+
 // A wave adds the rows of one chunk of sorted tokens, 512 columns of them, and gives
 // each id's sum to the gradient, or, where an id goes on in another chunk, to the
 // partial sums.  Chunks have the same number of tokens whatever their ids: one id
@@ -206,11 +235,11 @@ template <class X, class D>
 __global__ __launch_bounds__(256) void sum_kernel(const Sum p) {
   const int lane = threadIdx.x & 63;
   if (blockIdx.x >= p.sum_groups) {
-    const int64_t id = (blockIdx.x - p.sum_groups) * 4 + wave_id();
-    if (id >= p.vocab || p.starts[id] != p.starts[id + 1]) return;
-    const float none[8] = {};
-    auto* out = static_cast<typename Raw<D>::type*>(p.dtable) + id * p.lddtable;
-    for (int64_t c = lane * 8; c < p.d; c += 512) store_eight<D>(out + c, none, p.d - c);
+    const int64_t task = (blockIdx.x - p.sum_groups) * 4 + wave_id(), id = task / p.column_blocks;
+    if (id >= p.vocab) return;
+    const int slot = slot_of(static_cast<int>(id), p.shape);
+    if (p.starts[slot] != p.starts[slot + 1]) return;
+    clear<D>(p.dtable, id, task % p.column_blocks, p.d, p.lddtable);
     return;
   }
   const int64_t task = int64_t{blockIdx.x} * 4 + wave_id();
@@ -218,7 +247,7 @@ __global__ __launch_bounds__(256) void sum_kernel(const Sum p) {
   const int64_t chunk = task / p.column_blocks;
   const int64_t c = task % p.column_blocks * 512 + lane * 8;
   const int64_t left = p.d - c;
-  const int total = p.starts[p.vocab];
+  const int total = p.starts[p.shape.groups * p.shape.range];
   const int p0 = static_cast<int>(chunk) * p.chunk, p1 = min(p0 + p.chunk, total);
   if (p0 >= total) return;
   // lane i: the id of sorted token p0 - 1 + i
@@ -259,29 +288,31 @@ __global__ __launch_bounds__(256) void sum_kernel(const Sum p) {
 }
 
 // Adds the partial sums of the id that starts in a chunk and goes on behind it, in the
-// order of the chunks, cut into four stretches: a workgroup takes 1024 columns, 4 to a
+// order of the chunks, cut into kCuts stretches: a workgroup takes 1024 columns, 4 to a
 // lane, its waves 256 columns of a stretch each.
+constexpr int kCuts = 2;
 template <class D>
-__global__ __launch_bounds__(1024) void join_kernel(const Sum p) {
-  __shared__ f32x4 parts[4][256];
+__global__ __launch_bounds__(256 * kCuts) void join_kernel(const Sum p) {
+  __shared__ f32x4 parts[kCuts][256];
   const int64_t blocks = (p.d + 1023) / 1024;
   const int chunk = static_cast<int>(blockIdx.x / blocks);
-  const int total = p.starts[p.vocab];
+  const int total = p.starts[p.shape.groups * p.shape.range];
   const int p0 = chunk * p.chunk, p1 = p0 + p.chunk;
   if (p1 >= total) return;
   const int id = p.keys[p1 - 1];
-  const int first = p.starts[id], last = p.starts[id + 1];
+  const int slot = slot_of(id, p.shape);
+  const int first = p.starts[slot], last = p.starts[slot + 1];
   if (last <= p1 || first < p0) return;
   const int chunks = (last - 1) / p.chunk - chunk + 1;      // at least two
   const int lane = threadIdx.x & 63, wave = wave_id(), cut = wave >> 2;
   const int64_t c = blockIdx.x % blocks * 1024 + (wave & 3) * 256 + lane * 4;
-  const int each = (chunks + 3) / 4;
+  const int each = (chunks + kCuts - 1) / kCuts;
   const int from = cut * each, to = min(from + each, chunks);
   const int count = static_cast<int>(p.d - c < 4 ? p.d - c : 4);
   f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
   const float* at = p.partial + 2 * int64_t{chunk} * p.d + c;
   if (count == 4) {
-#pragma unroll 8
+#pragma unroll 16
     for (int k = from; k < to; ++k) sum += *reinterpret_cast<const f32x4_at4*>(at + (k == 0 ? 1 : 2 * int64_t{k}) * p.d);
   } else {
     for (int k = from; k < to; ++k)
@@ -299,7 +330,7 @@ __global__ __launch_bounds__(1024) void join_kernel(const Sum p) {
   for (int i = 0; i < 8; ++i) {
     out[i] = parts[0][2 * t + i / 4][i % 4];
 #pragma unroll
-    for (int s = 1; s < 4; ++s) out[i] += parts[s][2 * t + i / 4][i % 4];
+    for (int s = 1; s < kCuts; ++s) out[i] += parts[s][2 * t + i / 4][i % 4];
   }
   finish<D>(p, id, c8, p.d - c8, out);
 }
@@ -312,13 +343,14 @@ hipError_t launch_lookup(Lookup& p, int id_type, hipStream_t stream) {
 }
 
 template <class X, class D>
-hipError_t launch_sums(Sum& p, int64_t chunks, hipStream_t stream) {
-  const int64_t zero_groups = p.accumulate ? 0 : pieces_of(p.vocab, 4);
-  hipError_t e = hipSuccess;
-  if (p.sum_groups + zero_groups > 0)
-    e = queue(sum_kernel<X, D>, static_cast<unsigned>(p.sum_groups + zero_groups), 256, stream, p);
+hipError_t launch_sums(Sort& s, Sum& p, int64_t chunks, int id_type, hipStream_t stream) {
+  const unsigned groups = static_cast<unsigned>(s.shape.groups);
+  hipError_t e = id_type == OPT8_ID_INT32 ? queue(sort_kernel<int32_t>, groups, 64 * kSortWaves, stream, s)
+                                          : queue(sort_kernel<int64_t>, groups, 64 * kSortWaves, stream, s);
+  const int64_t sums = p.sum_groups + (p.accumulate ? 0 : pieces_of(p.vocab * p.column_blocks, 4));
+  if (e == hipSuccess && sums > 0) e = queue(sum_kernel<X, D>, static_cast<unsigned>(sums), 256, stream, p);
   if (e == hipSuccess && chunks > 1)
-    e = queue(join_kernel<D>, static_cast<unsigned>((chunks - 1) * pieces_of(p.d, 1024)), 1024, stream, p);
+    e = queue(join_kernel<D>, static_cast<unsigned>((chunks - 1) * pieces_of(p.d, 1024)), 256 * kCuts, stream, p);
   return e;
 }
 
@@ -353,18 +385,15 @@ hipError_t launch_embedding_backward(const opt8_embedding_grad& a, hipStream_t s
   s.ids = a.ids;
   s.tokens = a.tokens;
   s.vocab = a.vocab;
-  s.range = static_cast<int>(sort_range(a.vocab));
+  s.shape = sort_shape(a.vocab);
   s.order = reinterpret_cast<int*>(work + space.order);
   s.keys = reinterpret_cast<int*>(work + space.keys);
   s.starts = reinterpret_cast<int*>(work + space.starts);
-  const unsigned groups = static_cast<unsigned>(pieces_of(a.vocab, s.range));
-  const hipError_t e = a.id_type == OPT8_ID_INT32 ? queue(sort_kernel<int32_t>, groups, 64 * kSortWaves, stream, s)
-                                                  : queue(sort_kernel<int64_t>, groups, 64 * kSortWaves, stream, s);
-  if (e != hipSuccess) return e;
   Sum p;
   p.order = s.order;
   p.keys = s.keys;
   p.starts = s.starts;
+  p.shape = s.shape;
   p.dy = a.dy;
   p.dtable = a.dtable;
   p.partial = reinterpret_cast<float*>(work + space.partial);
@@ -380,9 +409,9 @@ hipError_t launch_embedding_backward(const opt8_embedding_grad& a, hipStream_t s
   p.tasks = chunks * p.column_blocks;
   p.sum_groups = pieces_of(p.tasks, 4);
   const bool wide = a.dtable_type == OPT8_TYPE_FP32;
-  if (a.type == OPT8_TYPE_BF16) return wide ? launch_sums<Bf16, float>(p, chunks, stream) : launch_sums<Bf16, Bf16>(p, chunks, stream);
-  if (a.type == OPT8_TYPE_FP16) return wide ? launch_sums<Fp16, float>(p, chunks, stream) : launch_sums<Fp16, Fp16>(p, chunks, stream);
-  return launch_sums<float, float>(p, chunks, stream);
+  if (a.type == OPT8_TYPE_BF16) return wide ? launch_sums<Bf16, float>(s, p, chunks, a.id_type, stream) : launch_sums<Bf16, Bf16>(s, p, chunks, a.id_type, stream);
+  if (a.type == OPT8_TYPE_FP16) return wide ? launch_sums<Fp16, float>(s, p, chunks, a.id_type, stream) : launch_sums<Fp16, Fp16>(s, p, chunks, a.id_type, stream);
+  return launch_sums<float, float>(s, p, chunks, a.id_type, stream);
 }
 
 }  // namespace opt8

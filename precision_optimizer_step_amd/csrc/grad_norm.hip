@@ -13,8 +13,8 @@ constexpr int kThreads = 256;
 constexpr int kPasses = OPT8_GRAD_PIECE / (kThreads * 8);    // 8 values to a thread in each
 
 struct NormOf {
-  const GradPiece* table;
-  int64_t pieces;
+  const GradPiece* pieces;    // behind the table's head
+  int64_t count;
   double* sums;       // [groups]
   double* squares;
   float* norm;
@@ -56,8 +56,10 @@ __device__ __forceinline__ void add_squares(const GradPiece& p, double* sum) {
 
 __global__ __launch_bounds__(kThreads) void squares_kernel(const NormOf p) {
   double sum[2] = {0.0, 0.0};
-  for (int64_t i = blockIdx.x; i < p.pieces; i += p.groups) {
-    const GradPiece piece = p.table[i];
+  GradPiece next = p.pieces[blockIdx.x];
+  for (int64_t i = blockIdx.x; i < p.count; i += p.groups) {
+    const GradPiece piece = next;
+    if (i + p.groups < p.count) next = p.pieces[i + p.groups];
     if (piece.type == OPT8_TYPE_BF16) add_squares<Bf16>(piece, sum);
     else if (piece.type == OPT8_TYPE_FP16) add_squares<Fp16>(piece, sum);
     else add_squares<float>(piece, sum);
@@ -81,8 +83,8 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const NormOf p) {
 }
 
 struct Clip {
-  const GradPiece* table;
-  int64_t pieces;
+  const GradPiece* pieces;    // behind the table's head
+  int64_t count;
   const double* squares;
   float* norm;
   double max_norm;
@@ -106,7 +108,7 @@ __device__ __forceinline__ void scaled(const GradPiece& p, float factor) {
     float out[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[i] = v[k][i] * factor;
-    if (at < p.count) store_eight<Y>(to + at, out, p.count - at);
+    if (at < p.count) stream_eight<Y>(to + at, out, p.count - at);
   }
 }
 
@@ -122,9 +124,10 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(const Clip p) {
   if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = static_cast<float>(norm);
   const double ratio = p.max_norm / (norm + 1e-6);
   const float factor = ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);    // NaN stays NaN
-  for (int64_t i = blockIdx.x; i < p.pieces; i += p.groups) {
-    const GradPiece piece = p.table[i];
-    if (factor == 1.0f && piece.from == piece.to) continue;
+  // pieces with a place of their own come first: all that there is to do by a factor of 1
+  const int64_t count = factor == 1.0f ? reinterpret_cast<const GradHead*>(p.pieces - 1)->own : p.count;
+  for (int64_t i = blockIdx.x; i < count; i += p.groups) {
+    const GradPiece piece = p.pieces[i];
     if (piece.type == OPT8_TYPE_BF16) scaled_to<Bf16>(piece, factor);
     else if (piece.type == OPT8_TYPE_FP16) scaled_to<Fp16>(piece, factor);
     else scaled_to<float>(piece, factor);
@@ -137,12 +140,12 @@ int groups_of(int64_t pieces) { return static_cast<int>(std::min<int64_t>(pieces
 
 hipError_t launch_grad_norm(const opt8_grads& a, hipStream_t stream) {
   NormOf p;
-  p.table = static_cast<const GradPiece*>(a.table);
-  p.pieces = a.pieces;
+  p.pieces = static_cast<const GradPiece*>(a.table) + 1;
+  p.count = a.table_bytes / OPT8_GRAD_PIECE_BYTES - 1;
   p.sums = static_cast<double*>(a.workspace);
   p.squares = a.squares;
   p.norm = a.norm;
-  p.groups = groups_of(a.pieces);
+  p.groups = groups_of(p.count);
   if (p.groups > 0) {
     const hipError_t e = queue(squares_kernel, static_cast<unsigned>(p.groups), kThreads, stream, p);
     if (e != hipSuccess) return e;
@@ -152,12 +155,12 @@ hipError_t launch_grad_norm(const opt8_grads& a, hipStream_t stream) {
 
 hipError_t launch_grad_clip(const opt8_grads& a, hipStream_t stream) {
   Clip p;
-  p.table = static_cast<const GradPiece*>(a.table);
-  p.pieces = a.pieces;
+  p.pieces = static_cast<const GradPiece*>(a.table) + 1;
+  p.count = a.table_bytes / OPT8_GRAD_PIECE_BYTES - 1;
   p.squares = a.squares;
   p.norm = a.norm;
   p.max_norm = a.max_norm;
-  p.groups = std::max(1, groups_of(a.pieces));
+  p.groups = std::max(1, groups_of(p.count));
   return queue(clip_kernel, static_cast<unsigned>(p.groups), kThreads, stream, p);
 }
 

@@ -11,8 +11,9 @@
 namespace opt8 {
 namespace {
 
-// 4 tokens x 512 columns to a wave of the lookup: 2^36 elements are 2^31 threads.
-constexpr int64_t kMaxLayerElements = int64_t{1} << 36;
+// 512 columns of a row to a wave of 64: 2^34 elements are 2^31 threads (rows of fewer
+// columns, at most 2^22, take a wave each).
+constexpr int64_t kMaxLayerElements = int64_t{1} << 34;
 
 bool wide_type(int type) { return type == OPT8_TYPE_BF16 || type == OPT8_TYPE_FP16 || type == OPT8_TYPE_FP32; }
 
@@ -39,7 +40,7 @@ int id_bytes(int id_type) { return id_type == OPT8_ID_INT32 ? 4 : 8; }
 int check_layers(const Matrix* list, int n) {
   for (int i = 0; i < n; ++i)
     if (list[i].p && list[i].rows * list[i].cols > kMaxLayerElements)
-      return refuse(OPT8_E_SIZE, "%s: over 2^36 elements", list[i].name);
+      return refuse(OPT8_E_SIZE, "%s: over 2^34 elements", list[i].name);
   return check_matrices(list, n);
 }
 
@@ -205,10 +206,10 @@ struct GradSpan {
 int grad_table(const opt8_grad* grads, int32_t n, void* table, int64_t bytes) {
   const int64_t pieces = grad_pieces(grads, n);
   if (pieces < 0) return static_cast<int>(pieces);
-  if (bytes < pieces * OPT8_GRAD_PIECE_BYTES)
+  const int64_t need = (pieces + 1) * OPT8_GRAD_PIECE_BYTES;
+  if (bytes < need)
     return refuse(OPT8_E_SIZE, "the table holds %lld bytes, %lld are needed", static_cast<long long>(bytes),
-                  static_cast<long long>(pieces * OPT8_GRAD_PIECE_BYTES));
-  if (pieces == 0) return OPT8_OK;
+                  static_cast<long long>(need));
   if (!table) return refuse(OPT8_E_NULL, "the table is NULL");
   try {
     std::vector<GradSpan> spans;
@@ -230,24 +231,30 @@ int grad_table(const opt8_grad* grads, int32_t n, void* table, int64_t bytes) {
   } catch (const std::bad_alloc&) {
     return refuse(OPT8_E_NOMEM, "out of host memory");
   }
-  char* at = static_cast<char*>(table);
-  for (int32_t i = 0; i < n; ++i) {
-    const opt8_grad& g = grads[i];
-    const bool own = g.out && g.out != g.grad;
-    char* from = static_cast<char*>(g.grad);
-    char* to = static_cast<char*>(own ? g.out : g.grad);
-    const int64_t size = type_bytes(g.type), to_size = type_bytes(own ? g.out_type : g.type);
-    for (int64_t first = 0; first < g.numel; first += OPT8_GRAD_PIECE) {
-      GradPiece piece;
-      piece.from = from + first * size;
-      piece.to = to + first * to_size;
-      piece.count = static_cast<int32_t>(std::min<int64_t>(OPT8_GRAD_PIECE, g.numel - first));
-      piece.type = static_cast<int16_t>(g.type);
-      piece.to_type = static_cast<int16_t>(own ? g.out_type : g.type);
-      std::memcpy(at, &piece, sizeof piece);
-      at += sizeof piece;
+  char* at = static_cast<char*>(table) + sizeof(GradHead);
+  GradHead head{pieces, 0, 0};
+  for (const bool own : {true, false}) {
+    for (int32_t i = 0; i < n; ++i) {
+      const opt8_grad& g = grads[i];
+      if (own != (g.out && g.out != g.grad)) continue;
+      char* from = static_cast<char*>(g.grad);
+      char* to = static_cast<char*>(own ? g.out : g.grad);
+      const int32_t to_type = own ? g.out_type : g.type;
+      const int64_t size = type_bytes(g.type), to_size = type_bytes(to_type);
+      for (int64_t first = 0; first < g.numel; first += OPT8_GRAD_PIECE) {
+        GradPiece piece;
+        piece.from = from + first * size;
+        piece.to = to + first * to_size;
+        piece.count = static_cast<int32_t>(std::min<int64_t>(OPT8_GRAD_PIECE, g.numel - first));
+        piece.type = static_cast<int16_t>(g.type);
+        piece.to_type = static_cast<int16_t>(to_type);
+        std::memcpy(at, &piece, sizeof piece);
+        at += sizeof piece;
+        head.own += own;
+      }
     }
   }
+  std::memcpy(table, &head, sizeof head);
   return OPT8_OK;
 }
 
@@ -255,14 +262,16 @@ int check_grads(const opt8_grads* a, bool norm) {
   clear_last_error();
   if (!a) return refuse(OPT8_E_NULL, "grads is NULL");
   int rc;
-  if ((rc = check_count("pieces", a->pieces, 0, kMaxPieces))) return rc;
+  if (a->table_bytes < OPT8_GRAD_PIECE_BYTES || a->table_bytes % OPT8_GRAD_PIECE_BYTES ||
+      a->table_bytes > (kMaxPieces + 1) * OPT8_GRAD_PIECE_BYTES)
+    return refuse(OPT8_E_SIZE, "a table has 24 bytes and 24 for each piece (got %lld)", static_cast<long long>(a->table_bytes));
   if (!norm && (!(a->max_norm >= 0.0) || !std::isfinite(a->max_norm)))
     return refuse(OPT8_E_HPARAM, "max_norm must be finite and not below 0");
-  if (!a->squares || (a->pieces > 0 && !a->table)) return refuse(OPT8_E_NULL, "table or squares is NULL");
+  if (!a->squares || !a->table) return refuse(OPT8_E_NULL, "table or squares is NULL");
   if (norm && (rc = check_workspace(a->workspace, a->workspace_bytes, OPT8_GRAD_WORKSPACE))) return rc;
-  if (a->pieces > 0 && reinterpret_cast<uintptr_t>(a->table) % 8) return refuse(OPT8_E_ALIGN, "table: not aligned to 8 bytes");
+  if (reinterpret_cast<uintptr_t>(a->table) % 8) return refuse(OPT8_E_ALIGN, "table: not aligned to 8 bytes");
   const Matrix list[] = {
-      {"table", a->pieces > 0 ? a->table : nullptr, a->pieces * OPT8_GRAD_PIECE_BYTES, 1, 1, 1, false, false},
+      {"table", a->table, a->table_bytes, 1, 1, 1, false, false},
       {"squares", a->squares, 1, 1, 1, 8, norm, false},
       {"norm", a->norm, 1, 1, 1, 4, true, false},
       workspace_of(norm ? a->workspace : nullptr, OPT8_GRAD_WORKSPACE),
@@ -302,7 +311,7 @@ extern "C" int64_t opt8_rms_norm_workspace(int64_t rows, int64_t d) {
 extern "C" int64_t opt8_grad_table_bytes(const opt8_grad* grads, int32_t n) {
   opt8::clear_last_error();
   const int64_t pieces = opt8::grad_pieces(grads, n);
-  return pieces < 0 ? pieces : pieces * OPT8_GRAD_PIECE_BYTES;
+  return pieces < 0 ? pieces : (pieces + 1) * OPT8_GRAD_PIECE_BYTES;
 }
 
 extern "C" int opt8_grad_table(const opt8_grad* grads, int32_t n, void* host_table, int64_t bytes) {

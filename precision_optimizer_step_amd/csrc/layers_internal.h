@@ -22,6 +22,14 @@ struct GradPiece {
 };
 static_assert(sizeof(GradPiece) == OPT8_GRAD_PIECE_BYTES, "the table's layout");
 
+// What stands before the pieces in a table.
+struct GradHead {
+  int64_t pieces;
+  int64_t own;       // of them with a place of their own for what is clipped: the first ones
+  int64_t reserved;
+};
+static_assert(sizeof(GradHead) == OPT8_GRAD_PIECE_BYTES, "the table's layout");
+
 // Each queues its launches for validated, non-empty arguments.
 hipError_t launch_embedding_forward(const opt8_embedding& a, hipStream_t stream);
 hipError_t launch_embedding_backward(const opt8_embedding_grad& a, hipStream_t stream);

@@ -63,17 +63,9 @@ struct Norm {
   float* scale;
   float* rstd;
   int64_t rows, d, ldx, ldresidual, ldsum, ldy, ldq;
-  int64_t groups;    // workgroups
   float eps, mean;   // mean: 1 / d
   int wide_weight;
 };
-
-// Workgroups go to the 8 XCDs in turn: each takes a run of neighbouring rows, so that
-// the scales of neighbouring rows, which share lines, meet in one L2.
-__device__ __forceinline__ int64_t run_of_rows(int64_t groups) {
-  const int64_t xcd = blockIdx.x & 7, q = groups >> 3, r = groups & 7;
-  return xcd * q + (xcd < r ? xcd : r) + (blockIdx.x >> 3);
-}
 
 // t of 8 columns, and its place in `sum`.
 template <class X>
@@ -88,7 +80,7 @@ __device__ __forceinline__ void norm_out(const Norm& p, int64_t row, int64_t c, 
   float n[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) n[i] = (t[i] * rstd) * w[i];
-  if (p.y && left > 0) store_eight<X>(static_cast<typename Raw<X>::type*>(p.y) + row * p.ldy + c, n, left);
+  if (p.y && left > 0) stream_eight<X>(static_cast<typename Raw<X>::type*>(p.y) + row * p.ldy + c, n, left);
   if constexpr (F >= 0) {
     float top = 0.0f;
 #pragma unroll
@@ -118,7 +110,7 @@ __global__ __launch_bounds__(256) void norm_kernel(const Norm p) {
   __shared__ float slots[4];
   typedef typename Raw<X>::type Value;
   const int l = threadIdx.x % LANES;
-  const int64_t row = run_of_rows(p.groups) * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t row = int64_t{blockIdx.x} * (256 / LANES) + threadIdx.x / LANES;
   const bool there = row < p.rows;
   Eight<X> x[K], r[K];
   float w[K][8], t[K][8];
@@ -144,7 +136,7 @@ __global__ __launch_bounds__(256) void norm_kernel(const Norm p) {
   for (int k = 0; k < K; ++k) {
     const int64_t c = (k * LANES + l) * 8, left = there ? p.d - c : 0;
     residual_sum<X>(p, x[k], r[k], t[k]);
-    if (p.sum && left > 0) store_eight<X>(static_cast<Value*>(p.sum) + row * p.ldsum + c, t[k], left);
+    if (p.sum && left > 0) stream_eight<X>(static_cast<Value*>(p.sum) + row * p.ldsum + c, t[k], left);
 #pragma unroll
     for (int i = 0; i < 8; ++i) squares = __builtin_fmaf(t[k][i], t[k][i], squares);
   }
@@ -162,7 +154,7 @@ template <class X, int F>
 __global__ __launch_bounds__(1024) void norm_long_kernel(const Norm p) {
   __shared__ float slots[16];
   typedef typename Raw<X>::type Value;
-  const int64_t row = run_of_rows(p.groups);
+  const int64_t row = blockIdx.x;
   const Value* xs = static_cast<const Value*>(p.x) + row * p.ldx;
   const Value* rs = static_cast<const Value*>(p.residual) + (p.residual ? row * p.ldresidual : 0);
   float squares = 0.0f;
@@ -190,15 +182,14 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const Norm p) {
       load_weight<X>(p.weight, p.wide_weight, c, left, w);
     }
     residual_sum<X>(p, x, r, t);
-    if (p.sum && left > 0) store_eight<X>(static_cast<Value*>(p.sum) + row * p.ldsum + c, t, left);
+    if (p.sum && left > 0) stream_eight<X>(static_cast<Value*>(p.sum) + row * p.ldsum + c, t, left);
     norm_out<X, F>(p, row, c, left, rstd, t, w);
   }
 }
 
 template <class X, int F, int LANES, int K>
 hipError_t launch_held(Norm& p, hipStream_t stream) {
-  p.groups = pieces_of(p.rows, 256 / LANES);
-  return queue(norm_kernel<X, F, LANES, K>, static_cast<unsigned>(p.groups), 256, stream, p);
+  return queue(norm_kernel<X, F, LANES, K>, static_cast<unsigned>(pieces_of(p.rows, 256 / LANES)), 256, stream, p);
 }
 
 template <class X, int F>
@@ -210,8 +201,7 @@ hipError_t launch_norm(Norm& p, hipStream_t stream) {
   if (p.d <= 4096) return launch_held<X, F, 256, 2>(p, stream);
   if (p.d <= 8192) return launch_held<X, F, 256, 4>(p, stream);
   if (p.d <= kNormHeld) return launch_held<X, F, 256, 8>(p, stream);
-  p.groups = p.rows;
-  return queue(norm_long_kernel<X, F>, static_cast<unsigned>(p.groups), 1024, stream, p);
+  return queue(norm_long_kernel<X, F>, static_cast<unsigned>(p.rows), 1024, stream, p);
 }
 
 template <class X>
@@ -315,7 +305,7 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_grad_kernel(co
             out[i] = at * __builtin_fmaf(-along, h[k][i], a[k][i]);
             if (p.dsum) out[i] += more[k][i];
           }
-          store_eight<X>(static_cast<Value*>(p.dx) + row * p.lddx + c, out, left);
+          stream_eight<X>(static_cast<Value*>(p.dx) + row * p.lddx + c, out, left);
         }
     }
   }
@@ -396,7 +386,7 @@ __global__ __launch_bounds__(1024) void dx_long_kernel(const NormGrad p) {
       out[i] = rstd * __builtin_fmaf(-along, x[i] * rstd, dy[i] * w[i]);
       if (p.dsum) out[i] += ds[i];
     }
-    store_eight<X>(static_cast<Value*>(p.dx) + row * p.lddx + c, out, p.d - c);
+    stream_eight<X>(static_cast<Value*>(p.dx) + row * p.lddx + c, out, p.d - c);
   }
 }
 
@@ -480,7 +470,6 @@ hipError_t launch_rms_norm_forward(const opt8_rms_norm& a, hipStream_t stream) {
   p.ldsum = a.ldsum;
   p.ldy = a.ldy;
   p.ldq = a.ldq;
-  p.groups = 0;
   p.eps = a.eps;
   p.mean = static_cast<float>(1.0 / static_cast<double>(a.d));
   p.wide_weight = a.weight_type == OPT8_TYPE_FP32 && a.type != OPT8_TYPE_FP32;

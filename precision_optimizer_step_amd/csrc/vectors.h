@@ -54,5 +54,21 @@ __device__ __forceinline__ void store_eight(typename Raw<X>::type* p, const floa
   else store_some(p, packed<X>(v), left);
 }
 
+// The same for results that leave in long streams: marked as not to be kept, they leave
+// the caches to what is read again (16384 embeddings of 4096 bf16 values with places:
+// 55 us without the mark, 39.5 with it).
+template <class X>
+__device__ __forceinline__ void stream_eight(typename Raw<X>::type* p, const float* v, int64_t left) {
+  if (left < 8) {
+    if constexpr (sizeof(typename Raw<X>::type) == 4) store_some(p, v, left);
+    else store_some(p, packed<X>(v), left);
+  } else if constexpr (sizeof(typename Raw<X>::type) == 4) {
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_at4*>(p));
+    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4_at4*>(p + 4));
+  } else {
+    __builtin_nontemporal_store(packed<X>(v), reinterpret_cast<i32x4_at2*>(p));
+  }
+}
+
 }  // namespace tile
 }  // namespace opt8

@@ -60,7 +60,7 @@ class opt8_grad(ctypes.Structure):
 
 
 class opt8_grads(_Descriptor):
-    _fields_ = [("table", _P), ("pieces", _L), ("squares", _P), ("norm", _P), ("workspace", _P), ("workspace_bytes", _L),
+    _fields_ = [("table", _P), ("table_bytes", _L), ("squares", _P), ("norm", _P), ("workspace", _P), ("workspace_bytes", _L),
                 ("max_norm", _D)]
 
 
@@ -287,17 +287,17 @@ def opt8_grad_table(grads, outs=None) -> torch.Tensor:
     size = fns["opt8_grad_table_bytes"](listed, len(grads))
     if size < 0:
         _check(int(size))
-    table = bytearray(max(1, size))
-    at = (ctypes.c_char * len(table)).from_buffer(table)
-    _check(fns["opt8_grad_table"](listed, len(grads), at, size))
-    return torch.frombuffer(table, dtype=torch.uint8, count=max(1, size))[:size].to(f"cuda:{device}")
+    table = bytearray(size)
+    _check(fns["opt8_grad_table"](listed, len(grads), (ctypes.c_char * size).from_buffer(table), size))
+    return torch.frombuffer(table, dtype=torch.uint8).to(f"cuda:{device}")
 
 
 def make_grads(table, squares, norm=None, workspace=None, max_norm=1.0) -> opt8_grads:
     """The list of a table for opt8_grad_norm and opt8_grad_clip: squares float64 [1], norm float32
     [1] or None, workspace (for opt8_grad_norm) a contiguous uint8 tensor of at least
-    OPT8_GRAD_WORKSPACE bytes, one for each call that may run at the same time."""
-    if table.dtype != torch.uint8 or table.dim() != 1 or not table.is_contiguous() or table.numel() % OPT8_GRAD_PIECE_BYTES:
+    OPT8_GRAD_WORKSPACE bytes, one for each call that may run at the same time.  The descriptor keeps
+    the table (the kernels go where it says)."""
+    if table.dtype != torch.uint8 or table.dim() != 1 or not table.is_contiguous():
         raise ValueError("table: expected what opt8_grad_table returned")
     _vector("squares", squares, (torch.float64,), 1)
     if norm is not None:
@@ -305,8 +305,10 @@ def make_grads(table, squares, norm=None, workspace=None, max_norm=1.0) -> opt8_
     if workspace is not None:
         _work(workspace)
     device = _placed(("squares", "table", "norm", "workspace"), (squares, table, norm, workspace))
-    return _on(device, opt8_grads(_ptr(table) or None, table.numel() // OPT8_GRAD_PIECE_BYTES, squares.data_ptr(), _ptr(norm),
+    desc = _on(device, opt8_grads(table.data_ptr(), table.numel(), squares.data_ptr(), _ptr(norm),
                                   _ptr(workspace), 0 if workspace is None else workspace.numel(), max_norm))
+    desc.kept = table
+    return desc
 
 
 # ----------------------------------------------------------------------------- calls
