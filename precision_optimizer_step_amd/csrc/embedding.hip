@@ -201,7 +201,7 @@ struct Sum {
   int64_t tasks;           // chunks * column blocks
   int64_t sum_groups;      // workgroups that add; those behind them store zeros
   float scale;
-  int column_blocks, chunk, accumulate;
+  int column_blocks, chunk, accumulate, stream;
 };
 
 // 8 columns of one row of the gradient.
@@ -254,19 +254,24 @@ __global__ __launch_bounds__(256) void sum_kernel(const Sum p) {
   const int at = p0 - 1 + lane;
   const int key = at >= 0 && at <= p1 && at < total ? p.keys[at] : -1;
   const int token = at >= p0 && at < p1 ? p.order[at] : 0;
-  const auto* dy = static_cast<const typename Raw<X>::type*>(p.dy) + c;
+  typedef typename Raw<X>::type Value;
+  const Value* dy = static_cast<const Value*>(p.dy) + c;
 
   bool shared = __builtin_amdgcn_readlane(key, 0) == __builtin_amdgcn_readlane(key, 1);
   float sum[8] = {};
   constexpr int kAhead = 8;
   for (int j0 = 0; j0 < p1 - p0; j0 += kAhead) {
     Eight<X> v[kAhead];
+    auto read = [&](auto&& one) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      v[u].zero();
-      const int64_t row = __builtin_amdgcn_readlane(token, min(j0 + u + 1, 63));
-      if (j0 + u < p1 - p0 && left > 0) v[u].load(dy + row * p.lddy, left);
-    }
+      for (int u = 0; u < kAhead; ++u) {
+        v[u].zero();
+        const int64_t row = __builtin_amdgcn_readlane(token, min(j0 + u + 1, 63));
+        if (j0 + u < p1 - p0 && left > 0) one(v[u], dy + row * p.lddy);
+      }
+    };
+    if (p.stream) read([&](Eight<X>& to, const Value* at) { to.stream(at, left); });
+    else read([&](Eight<X>& to, const Value* at) { to.load(at, left); });
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int j = j0 + u;
@@ -403,6 +408,7 @@ hipError_t launch_embedding_backward(const opt8_embedding_grad& a, hipStream_t s
   p.lddtable = a.lddtable;
   p.scale = a.scale;
   p.accumulate = a.accumulate != 0;
+  p.stream = streams(2 * a.d * (a.tokens + (p.accumulate ? a.tokens : a.vocab)));
   p.chunk = static_cast<int>(sum_chunk(a.tokens, a.d));
   p.column_blocks = static_cast<int>(pieces_of(a.d, 512));
   const int64_t chunks = pieces_of(a.tokens, p.chunk);

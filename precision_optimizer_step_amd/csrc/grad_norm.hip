@@ -19,6 +19,7 @@ struct NormOf {
   double* squares;
   float* norm;
   int groups;
+  int stream;
 };
 
 // Sum over a workgroup, in its first thread.
@@ -36,14 +37,19 @@ __device__ __forceinline__ double sum_of_group(double x) {
 
 // Squares in 64 bits: exact, and no gradient's is too large or too small for them.
 template <class X>
-__device__ __forceinline__ void add_squares(const GradPiece& p, double* sum) {
+__device__ __forceinline__ void add_squares(const GradPiece& p, bool stream, double* sum) {
   const auto* from = static_cast<const typename Raw<X>::type*>(p.from);
   Eight<X> v[kPasses];
+  if (stream && p.count == OPT8_GRAD_PIECE) {
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    const int at = (k * kThreads + static_cast<int>(threadIdx.x)) * 8;
-    v[k].zero();
-    if (at < p.count) v[k].load(from + at, p.count - at);
+    for (int k = 0; k < kPasses; ++k) v[k].stream(from + (k * kThreads + static_cast<int>(threadIdx.x)) * 8, 8);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+      const int at = (k * kThreads + static_cast<int>(threadIdx.x)) * 8;
+      v[k].zero();
+      if (at < p.count) v[k].load(from + at, p.count - at);
+    }
   }
 #pragma unroll
   for (int k = 0; k < kPasses; ++k)
@@ -60,9 +66,9 @@ __global__ __launch_bounds__(kThreads) void squares_kernel(const NormOf p) {
   for (int64_t i = blockIdx.x; i < p.count; i += p.groups) {
     const GradPiece piece = next;
     if (i + p.groups < p.count) next = p.pieces[i + p.groups];
-    if (piece.type == OPT8_TYPE_BF16) add_squares<Bf16>(piece, sum);
-    else if (piece.type == OPT8_TYPE_FP16) add_squares<Fp16>(piece, sum);
-    else add_squares<float>(piece, sum);
+    if (piece.type == OPT8_TYPE_BF16) add_squares<Bf16>(piece, p.stream, sum);
+    else if (piece.type == OPT8_TYPE_FP16) add_squares<Fp16>(piece, p.stream, sum);
+    else add_squares<float>(piece, p.stream, sum);
   }
   const double all = sum_of_group(sum[0] + sum[1]);
   if (threadIdx.x == 0) p.sums[blockIdx.x] = all;
@@ -146,6 +152,7 @@ hipError_t launch_grad_norm(const opt8_grads& a, hipStream_t stream) {
   p.squares = a.squares;
   p.norm = a.norm;
   p.groups = groups_of(p.count);
+  p.stream = streams(p.count * OPT8_GRAD_PIECE * 2);
   if (p.groups > 0) {
     const hipError_t e = queue(squares_kernel, static_cast<unsigned>(p.groups), kThreads, stream, p);
     if (e != hipSuccess) return e;

@@ -64,7 +64,7 @@ struct Norm {
   float* rstd;
   int64_t rows, d, ldx, ldresidual, ldsum, ldy, ldq;
   float eps, mean;   // mean: 1 / d
-  int wide_weight;
+  int wide_weight, stream;
 };
 
 // t of 8 columns, and its place in `sum`.
@@ -106,24 +106,29 @@ __device__ __forceinline__ void norm_out(const Norm& p, int64_t row, int64_t c, 
 // LANES lanes share a row and hold it in K pieces of 8 columns each, so that it is
 // read once.  F: codes of e4m3 (0), e5m2 (1) or none (-1).
 template <class X, int F, int LANES, int K>
-__global__ __launch_bounds__(256) void norm_kernel(const Norm p) {
-  __shared__ float slots[4];
+__global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_kernel(const Norm p) {
+  constexpr int kRows = LANES > 256 ? 1 : 256 / LANES;    // to a workgroup
+  __shared__ float slots[16];
   typedef typename Raw<X>::type Value;
   const int l = threadIdx.x % LANES;
-  const int64_t row = int64_t{blockIdx.x} * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t row = int64_t{blockIdx.x} * kRows + threadIdx.x / LANES;
   const bool there = row < p.rows;
   Eight<X> x[K], r[K];
   float w[K][8], t[K][8];
+  auto read = [&](auto&& one) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int64_t c = (k * LANES + l) * 8, left = there ? p.d - c : 0;
-    x[k].zero();
-    r[k].zero();
-    if (left > 0) {
-      x[k].load(static_cast<const Value*>(p.x) + row * p.ldx + c, left);
-      if (p.residual) r[k].load(static_cast<const Value*>(p.residual) + row * p.ldresidual + c, left);
+    for (int k = 0; k < K; ++k) {
+      const int64_t c = (k * LANES + l) * 8, left = there ? p.d - c : 0;
+      x[k].zero();
+      r[k].zero();
+      if (left > 0) {
+        one(x[k], static_cast<const Value*>(p.x) + row * p.ldx + c, left);
+        if (p.residual) one(r[k], static_cast<const Value*>(p.residual) + row * p.ldresidual + c, left);
+      }
     }
-  }
+  };
+  if (p.stream) read([](Eight<X>& v, const Value* at, int64_t left) { v.stream(at, left); });
+  else read([](Eight<X>& v, const Value* at, int64_t left) { v.load(at, left); });
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int64_t c = (k * LANES + l) * 8;
@@ -189,7 +194,8 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const Norm p) {
 
 template <class X, int F, int LANES, int K>
 hipError_t launch_held(Norm& p, hipStream_t stream) {
-  return queue(norm_kernel<X, F, LANES, K>, static_cast<unsigned>(pieces_of(p.rows, 256 / LANES)), 256, stream, p);
+  constexpr int kThreads = LANES > 256 ? LANES : 256;
+  return queue(norm_kernel<X, F, LANES, K>, static_cast<unsigned>(pieces_of(p.rows, kThreads / LANES)), kThreads, stream, p);
 }
 
 template <class X, int F>
@@ -200,7 +206,7 @@ hipError_t launch_norm(Norm& p, hipStream_t stream) {
   if (p.d <= 2048) return launch_held<X, F, 256, 1>(p, stream);
   if (p.d <= 4096) return launch_held<X, F, 256, 2>(p, stream);
   if (p.d <= 8192) return launch_held<X, F, 256, 4>(p, stream);
-  if (p.d <= kNormHeld) return launch_held<X, F, 256, 8>(p, stream);
+  if (p.d <= kNormHeld) return launch_held<X, F, 512, 4>(p, stream);
   return queue(norm_long_kernel<X, F>, static_cast<unsigned>(p.rows), 1024, stream, p);
 }
 
@@ -223,7 +229,7 @@ struct NormGrad {
   int64_t rows, d, lddy, ldx, lddsum, lddx;
   int groups;
   float mean;
-  int wide_weight, wide_dweight;
+  int wide_weight, wide_dweight, stream;
 };
 
 // Sums of dweight's columns, rounded (a lone workgroup) or left to the second kernel.
@@ -257,7 +263,7 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_grad_kernel(co
   Eight<X> dy[K], x[K], ds[K];
   float rstd = 0.0f;
   const int64_t step = int64_t{p.groups} * kRows;
-  auto load = [&](int64_t row) {
+  auto read = [&](int64_t row, auto&& one) {
     const bool there = row < p.rows;
     rstd = there ? p.rstd[row] : 0.0f;
 #pragma unroll
@@ -267,11 +273,15 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_grad_kernel(co
       x[k].zero();
       ds[k].zero();
       if (left > 0) {
-        dy[k].load(static_cast<const Value*>(p.dy) + row * p.lddy + c, left);
-        x[k].load(static_cast<const Value*>(p.x) + row * p.ldx + c, left);
-        if (p.dsum) ds[k].load(static_cast<const Value*>(p.dsum) + row * p.lddsum + c, left);
+        one(dy[k], static_cast<const Value*>(p.dy) + row * p.lddy + c, left);
+        one(x[k], static_cast<const Value*>(p.x) + row * p.ldx + c, left);
+        if (p.dsum) one(ds[k], static_cast<const Value*>(p.dsum) + row * p.lddsum + c, left);
       }
     }
+  };
+  auto load = [&](int64_t row) {
+    if (p.stream) read(row, [](Eight<X>& v, const Value* at, int64_t left) { v.stream(at, left); });
+    else read(row, [](Eight<X>& v, const Value* at, int64_t left) { v.load(at, left); });
   };
   load(int64_t{blockIdx.x} * kRows + g);
   int turn = 0;
@@ -473,6 +483,7 @@ hipError_t launch_rms_norm_forward(const opt8_rms_norm& a, hipStream_t stream) {
   p.eps = a.eps;
   p.mean = static_cast<float>(1.0 / static_cast<double>(a.d));
   p.wide_weight = a.weight_type == OPT8_TYPE_FP32 && a.type != OPT8_TYPE_FP32;
+  p.stream = streams(a.rows * a.d * (a.residual ? 6 : 4));
   if (a.type == OPT8_TYPE_BF16) return launch_codes<Bf16>(p, a.q_type, stream);
   if (a.type == OPT8_TYPE_FP16) return launch_codes<Fp16>(p, a.q_type, stream);
   return launch_codes<float>(p, a.q_type, stream);
@@ -498,6 +509,7 @@ hipError_t launch_rms_norm_backward(const opt8_rms_norm_grad& a, hipStream_t str
   p.mean = static_cast<float>(1.0 / static_cast<double>(a.d));
   p.wide_weight = a.weight_type == OPT8_TYPE_FP32 && a.type != OPT8_TYPE_FP32;
   p.wide_dweight = a.dweight_type == OPT8_TYPE_FP32 && a.type != OPT8_TYPE_FP32;
+  p.stream = streams(a.rows * a.d * (a.dsum ? 8 : 6));
   if (a.type == OPT8_TYPE_BF16) return launch_grad<Bf16>(p, stream);
   if (a.type == OPT8_TYPE_FP16) return launch_grad<Fp16>(p, stream);
   return launch_grad<float>(p, stream);

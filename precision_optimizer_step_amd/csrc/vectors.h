@@ -25,6 +25,12 @@ struct Eight {
       for (int i = 0; i < 8; ++i) v[i] = i < left ? static_cast<short>(p[i]) : 0;
     }
   }
+  // The same for values that are read once, by a call too large for the caches to keep
+  // any of it (streams() below): past them.
+  __device__ __forceinline__ void stream(const uint16_t* p, int64_t left) {
+    if (left >= 8) v = __builtin_bit_cast(i16x8, static_cast<i32x4>(__builtin_nontemporal_load(reinterpret_cast<const i32x4_at2*>(p))));
+    else load(p, left);
+  }
   __device__ __forceinline__ float operator[](int i) const { return value_of<X>(static_cast<uint16_t>(v[i])); }
 };
 template <>
@@ -44,6 +50,8 @@ struct Eight<float> {
       for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
     }
   }
+  // (through the caches: a lane's 32 bytes are two loads, which share every line)
+  __device__ __forceinline__ void stream(const float* p, int64_t left) { load(p, left); }
   __device__ __forceinline__ float operator[](int i) const { return v[i]; }
 };
 
@@ -54,19 +62,18 @@ __device__ __forceinline__ void store_eight(typename Raw<X>::type* p, const floa
   else store_some(p, packed<X>(v), left);
 }
 
-// The same for results that leave in long streams: marked as not to be kept, they leave
-// the caches to what is read again (16384 embeddings of 4096 bf16 values with places:
-// 55 us without the mark, 39.5 with it).
+// The same for results that leave in long streams: 16-bit ones are marked as not to be
+// kept and leave the caches to what is read again (16384 embeddings of 4096 bf16 values
+// with places: 55 us without the mark, 39.5 with it).  32-bit ones are not: a lane's
+// 32 bytes are two stores to a line, which meet in a cache (gradient of 50257 x 2048
+// fp32 embeddings: 147 us, with the mark 203).
 template <class X>
 __device__ __forceinline__ void stream_eight(typename Raw<X>::type* p, const float* v, int64_t left) {
-  if (left < 8) {
-    if constexpr (sizeof(typename Raw<X>::type) == 4) store_some(p, v, left);
-    else store_some(p, packed<X>(v), left);
-  } else if constexpr (sizeof(typename Raw<X>::type) == 4) {
-    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_at4*>(p));
-    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4_at4*>(p + 4));
+  if constexpr (sizeof(typename Raw<X>::type) == 4) {
+    store_some(p, v, left);
   } else {
-    __builtin_nontemporal_store(packed<X>(v), reinterpret_cast<i32x4_at2*>(p));
+    if (left < 8) store_some(p, packed<X>(v), left);
+    else __builtin_nontemporal_store(packed<X>(v), reinterpret_cast<i32x4_at2*>(p));
   }
 }
 
