@@ -28,7 +28,10 @@ struct Lookup {
 };
 
 // A wave takes 512 columns of kTokens tokens, 8 columns to a lane.  One load brings the
-// tokens' ids and one their places (a lane each), the next ones all rows.
+// tokens' ids and one their places (a lane each), the next ones all rows.  Bound by
+// memory: 16384 tokens of 4096 bf16 values with places 39 us, 256 MB of them read and
+// written (rows of frequent ids once by each XCD's L2) at 6.6 TB/s; with one token to a
+// wave 41, with four 39.6.
 constexpr int kTokens = 2;
 template <class X, class Id>
 __global__ __launch_bounds__(256) void lookup_kernel(const Lookup p) {
@@ -73,8 +76,10 @@ __device__ __forceinline__ int slot_of(int id, const SortShape& s) { return (id 
 // owns a share of the ids and reads all tokens, counting its own ones and noting where
 // they stand, and then gives them their positions.  Waves read consecutive stretches,
 // and each has its own counter for every id, so that a token's position depends on the
-// ids alone.  A wave that finds more than it can note (an id with a sixteenth of over
-// 2^13 tokens) reads its stretch again.
+// ids alone.  A wave that finds more than it can note (where one id has over 512 of its
+// stretch's tokens) reads its stretch again.  256 workgroups read 16384 ids in 9.4 us,
+// 1001 in 5.8; with an adjacent range of ids to each, where a few workgroups have the
+// frequent ones, 94 and 10.5.
 struct Sort {
   const void* ids;
   int64_t tokens, vocab;
@@ -230,7 +235,10 @@ __device__ __forceinline__ void clear(void* dtable, int64_t row, int64_t block, 
 // A wave adds the rows of one chunk of sorted tokens, 512 columns of them, and gives
 // each id's sum to the gradient, or, where an id goes on in another chunk, to the
 // partial sums.  Chunks have the same number of tokens whatever their ids: one id
-// with half of the tokens costs no more than as many different ones.
+// with half of the tokens costs no more than as many different ones.  Waves behind them
+// clear the rows without tokens, 1 KB each in the order of the addresses (with a row of
+// 8 KB to a wave the clearing runs at 5.5 TB/s instead of 6.7).  Bound by memory: 12288 of
+// 16384 tokens into 50257 x 4096 bf16, 518 MB in 75 us (6.9 TB/s).
 template <class X, class D>
 __global__ __launch_bounds__(256) void sum_kernel(const Sum p) {
   const int lane = threadIdx.x & 63;
@@ -294,7 +302,9 @@ __global__ __launch_bounds__(256) void sum_kernel(const Sum p) {
 
 // Adds the partial sums of the id that starts in a chunk and goes on behind it, in the
 // order of the chunks, cut into kCuts stretches: a workgroup takes 1024 columns, 4 to a
-// lane, its waves 256 columns of a stretch each.
+// lane, its waves 256 columns of a stretch each.  Mostly the time to find that there is
+// little to do (6 us of the case above); with one, two and four stretches 65536 tokens of
+// 1024 columns took 99.1, 97.6 and 100.6 us in all, 16384 of one id 88.7, 84.3 and 84.6.
 constexpr int kCuts = 2;
 template <class D>
 __global__ __launch_bounds__(256 * kCuts) void join_kernel(const Sum p) {

@@ -36,7 +36,7 @@ inline SortShape sort_shape(int64_t vocab) {
 
 // Sorted tokens that a wave adds up: 32 where that leaves at least 4096 waves (4 to a
 // SIMD), fewer for short batches; at most 32 (a wave keeps a chunk's tokens and its two
-// neighbours in its lanes).
+// neighbours in its lanes).  Not fitted: the waves' count is the reason.
 inline int64_t sum_chunk(int64_t tokens, int64_t d) {
   const int64_t waves = tokens * pieces_of(d, 512);
   return waves >= 32 * 4096 ? 32 : waves >= 16 * 4096 ? 16 : 8;

@@ -99,6 +99,8 @@ def _functions():
 
 # ----------------------------------------------------------------------------- checks
 def _vector(what, t, dtypes, n):
+    if t.shape == (n,) and t.dtype in dtypes and t.is_contiguous():
+        return
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: dtype {t.dtype} not allowed here (expected one of "
                          f"{', '.join(str(d) for d in dtypes)})")

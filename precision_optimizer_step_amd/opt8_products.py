@@ -95,6 +95,8 @@ def _matrix(what, t, dtypes, rows, cols, owned=False):
     """The row distance of a [rows, cols] torch matrix with dense rows.  owned: the
     last row's last 16 bytes must belong to the tensor's storage whole (the library
     reads rows in pieces of 16)."""
+    if t.shape == (rows, cols) and t.dtype in dtypes and t.is_contiguous() and not (owned and cols * t.element_size() % 16):
+        return cols      # the usual case, in a third of the time
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: dtype {t.dtype} not allowed here (expected one of "
                          f"{', '.join(str(d) for d in dtypes)})")
@@ -118,6 +120,8 @@ def _matrix(what, t, dtypes, rows, cols, owned=False):
 
 
 def _scales(what, t, blocks, across):
+    if t.dtype == torch.float32 and t.shape == (blocks, across) and t.is_contiguous():
+        return
     if t.dtype != torch.float32:
         raise ValueError(f"{what}: dtype {t.dtype} not allowed here (expected torch.float32)")
     if t.shape != (blocks, across):
@@ -129,9 +133,10 @@ def _scales(what, t, blocks, across):
 def _placed(names, tensors):
     """The one GPU that all are on, and that one current (a call queues on the current device)."""
     first = tensors[0].get_device()
-    for i, t in enumerate(tensors):
+    for t in tensors:
         if t is not None and t.get_device() != first:
-            raise ValueError(f"{names[i]}: on {t.device}, but {names[0]} is on {tensors[0].device}")
+            name = names[next(i for i, other in enumerate(tensors) if other is t)]
+            raise ValueError(f"{name}: on {t.device}, but {names[0]} is on {tensors[0].device}")
     if first < 0:
         raise ValueError(f"{names[0]}: on {tensors[0].device}; the operators run on a GPU")
     if first != torch.cuda.current_device():
