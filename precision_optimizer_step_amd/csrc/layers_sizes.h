@@ -36,7 +36,10 @@ inline SortShape sort_shape(int64_t vocab) {
 
 // Sorted tokens that a wave adds up: 32 where that leaves at least 4096 waves (4 to a
 // SIMD), fewer for short batches; at most 32 (a wave keeps a chunk's tokens and its two
-// neighbours in its lanes).  Not fitted: the waves' count is the reason.
+// neighbours in its lanes).  Measured, whole calls in us with chunks of 8, 16 and 32
+// (50257 ids, bf16):  1001 x 1600: 16.1 19.7 27.4   4096 x 1024: 20.8 25.3 33.5
+//   4096 x 4096: 27.7 29.2 35.6   16384 x 1024: 36.0 35.4 40.6   8192 x 4096: 48.0 44.5 49.1
+//   65536 x 1024: 99.3 85.2 80.1   16384 x 4096: 101.8 97.3 95.3
 inline int64_t sum_chunk(int64_t tokens, int64_t d) {
   const int64_t waves = tokens * pieces_of(d, 512);
   return waves >= 32 * 4096 ? 32 : waves >= 16 * 4096 ? 16 : 8;
