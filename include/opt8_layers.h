@@ -45,7 +45,7 @@ typedef enum {
 /* y[i] = scale * table[ids[i]] + place_table[place_ids[i]]: in fp32, rounded once
  * for the product with scale and once for the sum, then to the type.  An id that is
  * no row of its table (a padding of -1) stands for a row of zeros.  place_ids and
- * place_table are NULL where there are no places. */
+ * place_table are NULL where there are no places.  A table without rows may be NULL. */
 typedef struct opt8_embedding {
   const void* ids;           /* [tokens]                                             */
   const void* table;         /* [vocab, d]                                           */
@@ -95,7 +95,7 @@ int64_t opt8_embedding_workspace(int64_t tokens, int64_t vocab, int64_t d);
  *   q, scale   codes of n and their scales, as opt8_fp8_quantize gives them by rows
  *         (OPT8_FP8_BLOCK_ROW; scale [ceil(d/128), rows]): operand a of opt8_fp8_matmul
  *   rstd  fp32 [rows], for the backward pass
- * The mean is an fp32 sum of squares: t's square has to stay below 2^128.  sum may
+ * The mean is an fp32 sum of squares, which has to stay below 2^128 (beyond it rstd is 0).  sum may
  * be the same matrix as residual or x (the same address and ld). */
 typedef struct opt8_rms_norm {
   const void* x;             /* [rows, d]                                            */

@@ -68,9 +68,15 @@ __global__ __launch_bounds__(256) void lookup_kernel(const Lookup p) {
 }
 
 // ---------------------------------------------------------------- gradient
-// Where an id's tokens start among the sorted ones stands in starts[slot_of(id)], and
-// where they end in the next place: id / groups within the workgroup's ids.
-__device__ __forceinline__ int slot_of(int id, const SortShape& s) { return (id & (s.groups - 1)) * s.range + (id >> s.shift); }
+// An id is the (id / groups)-th of its workgroup's.  The workgroup is id modulo groups,
+// moved on with every round: neither neighbours nor multiples of a power of two, which
+// ids in use together often are, fall to one.
+constexpr int kTurn = 37;
+__device__ __forceinline__ int owner_of(int id, const SortShape& s) { return (id + (id >> s.shift) * kTurn) & (s.groups - 1); }
+__device__ __forceinline__ int id_of(int owner, int own, const SortShape& s) { return own << s.shift | ((owner - own * kTurn) & (s.groups - 1)); }
+// Where its tokens start among the sorted ones stands in starts[slot_of(id)], and where
+// they end in the next place.
+__device__ __forceinline__ int slot_of(int id, const SortShape& s) { return owner_of(id, s) * s.range + (id >> s.shift); }
 
 // The tokens sorted by their id's slot, those of one id by their place: a workgroup
 // owns a share of the ids and reads all tokens, counting its own ones and noting where
@@ -98,7 +104,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_kernel(const Sort p) {
   constexpr int kPlaceBits = 19;
   static_assert(kSortRange <= 1 << (31 - kPlaceBits) && (1 << 22) / kSortWaves + 64 <= 1 << kPlaceBits, "a note's bits");
   const int t = threadIdx.x, lane = t & 63, wave = wave_id();
-  const int group = static_cast<int>(blockIdx.x), mask = p.shape.groups - 1, shift = p.shape.shift, range = p.shape.range;
+  const int group = static_cast<int>(blockIdx.x), range = p.shape.range;
   for (int i = t; i < range * kSortWaves; i += kThreads) count[i] = 0;
   __syncthreads();
 
@@ -115,12 +121,12 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_kernel(const Sort p) {
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int owner = id[u] < 0 ? p.shape.groups : id[u] & mask;
+      const int owner = id[u] < 0 ? p.shape.groups : owner_of(id[u], p.shape);
       below += owner < group;
       const uint64_t mine = __ballot(owner == group);
       if (mine == 0) continue;
       if (owner == group) {
-        const int own = id[u] >> shift, at = found + __builtin_popcountll(mine & under);
+        const int own = id[u] >> p.shape.shift, at = found + __builtin_popcountll(mine & under);
         atomicAdd(&count[own * kSortWaves + wave], 1);
         if (at < kNoted) noted[wave][at] = own << kPlaceBits | static_cast<int>(i0 - begin + 64 * u + lane);
       }
@@ -158,7 +164,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_kernel(const Sort p) {
     if (i % kSortWaves == 0) p.starts[group * range + i / kSortWaves] = at;
     at += n;
   }
-  if (t == 0 && group == mask) p.starts[p.shape.groups * range] = total;
+  if (t == 0 && group == p.shape.groups - 1) p.starts[p.shape.groups * range] = total;
   __syncthreads();
 
   // Positions for 64 tokens of the wave's, in their order: own < 0 where there is none.
@@ -172,7 +178,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_kernel(const Sort p) {
       if (own == one) {
         const int to = first + __builtin_popcountll(same & under);
         p.order[to] = static_cast<int>(token);
-        p.keys[to] = one << shift | group;
+        p.keys[to] = id_of(group, one, p.shape);
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       if (lane == 0) *next = first + __builtin_popcountll(same);
@@ -189,7 +195,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_kernel(const Sort p) {
     for (int64_t i0 = begin; i0 < end; i0 += 64) {
       const int64_t i = i0 + lane;
       const int id = i < end ? row_of<Id>(p.ids, i, p.vocab) : -1;
-      place(id >= 0 && (id & mask) == group ? id >> shift : -1, i);
+      place(id >= 0 && owner_of(id, p.shape) == group ? id >> p.shape.shift : -1, i);
     }
   }
 }

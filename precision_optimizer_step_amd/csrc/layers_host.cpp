@@ -66,15 +66,16 @@ int embedding_forward(const opt8_embedding* a, void* hip_stream) {
     return rc;
   if (!std::isfinite(a->scale)) return refuse(OPT8_E_HPARAM, "scale is not finite");
   if (a->tokens == 0 || a->d == 0) return OPT8_OK;
-  if (!a->place_ids != !a->place_table) return refuse(OPT8_E_NULL, "place_ids and place_table go together");
-  if (a->place_table && (rc = check_count("places", a->places, 0, kMaxCount))) return rc;
+  if (a->place_ids && (rc = check_count("places", a->places, 0, kMaxCount))) return rc;
+  if (a->place_ids ? !a->place_table && a->places > 0 : a->place_table != nullptr)
+    return refuse(OPT8_E_NULL, "place_ids and place_table go together");
   if (!a->ids || !a->y || (a->vocab > 0 && !a->table)) return refuse(OPT8_E_NULL, "ids, table or y is NULL");
   const int size = type_bytes(a->type), id = id_bytes(a->id_type);
   const Matrix list[] = {
       {"ids", a->ids, a->tokens, 1, 1, id, false, false},
       {"table", a->vocab > 0 ? a->table : nullptr, a->vocab, a->d, a->ldtable, size, false, false},
       {"place_ids", a->place_ids, a->tokens, 1, 1, id, false, false},
-      {"place_table", a->places > 0 ? a->place_table : nullptr, a->places, a->d, a->ldplace, size, false, false},
+      {"place_table", a->place_ids && a->places > 0 ? a->place_table : nullptr, a->places, a->d, a->ldplace, size, false, false},
       {"y", a->y, a->tokens, a->d, a->ldy, size, true, false},
   };
   if ((rc = check_layers(list, 5))) return rc;

@@ -19,7 +19,7 @@ inline int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 inline bool streams(int64_t bytes) { return bytes > int64_t{128} << 20; }
 
 // ---------------------------------------------------------------- embedding's gradient
-// The sort's workgroups, a power of two: workgroup w owns the ids w, w + groups, ...
+// The sort's workgroups, a power of two: each owns one of every `groups` ids in a row
 // (so that ids next to each other, which are often the frequent ones, are not one
 // workgroup's), at most kSortRange of them, counted in LDS.
 constexpr int kSortWaves = 16;

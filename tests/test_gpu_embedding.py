@@ -28,6 +28,8 @@ def values(rows, cols, dtype, g, extra=0, head=0, scale=1.0):
 def some_ids(n, vocab, g, kind="even"):
     if kind == "one":
         return torch.full((n,), vocab // 2, dtype=I64)
+    if kind == "multiples":    # of the number of the sort's workgroups
+        return torch.randint(0, vocab // 256, (n,), generator=g) * 256
     if kind == "frequent":
         return (torch.exp(torch.rand(n, generator=g, dtype=torch.float64) * torch.log(torch.tensor(vocab + 1.0))).long() - 1).clamp(0, vocab - 1)
     ids = torch.randint(0, vocab, (n,), generator=g)
@@ -67,6 +69,8 @@ def test_lookup_without_a_vocabulary_gives_zeros_and_places():
     assert bool((y == 0).all())
     ops.opt8_embedding_forward(ops.make_embedding(ids, torch.empty(0, 40, device="cuda"), y, place_ids=ids + 2, place_table=p))
     assert torch.equal(y, p[2].expand(5, 40))
+    ops.opt8_embedding_forward(ops.make_embedding(ids + 1, p, y, place_ids=ids, place_table=torch.empty(0, 40, device="cuda")))
+    assert torch.equal(y, p[1].expand(5, 40))
 
 
 def test_rows_beside_the_tokens_do_not_count():
@@ -115,6 +119,7 @@ def test_gradient(tokens, vocab, d, kind, dtype, out):
     (8191, 50257, 64, "frequent"), (20000, 1000, 40, "frequent"),   # chunks of 8 tokens, and ids over several of them
     (32768, 300, 1024, "even"), (70000, 90, 513, "frequent"),       # chunks of 16 and of 32
     (20000, 300000, 24, "even"),                                    # more ids than 256 workgroups count
+    (9000, 50257, 16, "multiples"), (9000, 300000, 16, "multiples"),
     (9000, 4, 16, "one"), (200000, 5, 8, "one")])                   # more of one id than a wave notes
 def test_gradient_of_many_tokens(tokens, vocab, d, kind):
     gradient(tokens, vocab, d, F32, kind=kind)

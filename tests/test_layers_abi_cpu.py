@@ -200,7 +200,8 @@ def test_calls_that_take_an_operand_s_place(L):
 def test_empty_calls_are_no_ops(L):
     none = dict(ids=None, table=None, y=None, place_ids=None, place_table=None)
     assert embed(tokens=0, **none) == opt8.OPT8_OK and embed(d=0, **none) == opt8.OPT8_OK
-    assert embed(vocab=0, table=None) in REACHED
+    assert embed(vocab=0, table=None) in REACHED and embed(places=0, place_table=None) in REACHED
+    assert embed(place_ids=None, place_table=None, places=-7) in REACHED       # read with place_ids only
     assert embed_grad(vocab=0, dtable=None, workspace=None) == opt8.OPT8_OK
     assert embed_grad(tokens=0, accumulate=1, ids=None, dy=None, dtable=None, workspace=None) == opt8.OPT8_OK
     assert embed_grad(tokens=0, ids=None, dy=None) in REACHED
