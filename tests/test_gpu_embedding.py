@@ -125,6 +125,18 @@ def test_gradient_of_many_tokens(tokens, vocab, d, kind):
     gradient(tokens, vocab, d, F32, kind=kind)
 
 
+@pytest.mark.parametrize("vocab,d,kind", [(1 << 22, 2, "frequent"), (1 << 22, 1, "even"), (3, 8, "one")])
+def test_the_most_tokens(vocab, d, kind):
+    """2^22 of them, into as many rows or into one."""
+    gradient(1 << 22, vocab, d, BF, F32, kind=kind)
+    lookup(1 << 22, vocab, d, BF, kind=kind)
+
+
+def test_the_widest_rows():
+    lookup(3, 5, 1 << 20, BF, places=2)
+    gradient(11, 5, 1 << 20, BF, kind="outside")
+
+
 def test_gradient_without_tokens_is_zero_or_what_it_was():
     ids, dy = torch.empty(0, dtype=I64, device="cuda"), torch.empty(0, 70, dtype=BF, device="cuda")
     work = torch.empty(ops.opt8_embedding_workspace(0, 33, 70), dtype=torch.uint8, device="cuda")

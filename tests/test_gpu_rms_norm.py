@@ -171,6 +171,12 @@ def test_dx_in_an_operand_s_place(d, where):
     backward(1300 if d < 5000 else 20, d, BF, in_place=where)
 
 
+@pytest.mark.parametrize("rows,d", [(1 << 22, 3), (2, 1 << 20)])
+def test_the_most_and_the_widest_rows(rows, d):
+    forward(rows, d, BF, kind=E5)
+    backward(rows, d, BF, out=F32)
+
+
 def test_backward_gives_the_same_bits():
     a, b = backward(3000, 200, F32), backward(3000, 200, F32)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
