@@ -201,6 +201,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_kernel(const Sort p) {
 }
 
 struct Sum {
+  const void* ids;
   const int* order;
   const int* keys;
   const int* starts;
@@ -208,8 +209,8 @@ struct Sum {
   const void* dy;
   void* dtable;
   float* partial;    // [chunk][2][d]
-  int64_t vocab, d, lddy, lddtable;
-  int64_t tasks;           // chunks * column blocks
+  int64_t tokens, vocab, d, lddy, lddtable;
+  int64_t tasks;           // chunks (or tokens) * column blocks
   int64_t sum_groups;      // workgroups that add; those behind them store zeros
   float scale;
   int column_blocks, chunk, accumulate, stream;
@@ -236,6 +237,57 @@ __device__ __forceinline__ void clear(void* dtable, int64_t row, int64_t block, 
   const float none[8] = {};
   const int64_t c = block * 512 + (threadIdx.x & 63) * 8;
   if (c < d) stream_eight<D>(static_cast<typename Raw<D>::type*>(dtable) + row * ld + c, none, d - c);
+}
+
+// At most kFewTokens tokens, without a sort: a wave takes 512 columns of one token, holds
+// all ids in its lanes, and if no token before its own has the same id, it adds the rows
+// of all that have, in their order.  Waves behind those clear the rows without tokens
+// (50257 x 4096 bf16 in 57 us with the call's launch, 7.2 TB/s).
+template <class X, class D, class Id>
+__global__ __launch_bounds__(256) void few_kernel(const Sum p) {
+  static_assert(kFewTokens <= 128, "two ids to a lane");
+  typedef typename Raw<X>::type Value;
+  const int lane = threadIdx.x & 63;
+  const int a = lane < p.tokens ? row_of<Id>(p.ids, lane, p.vocab) : -1;
+  const int b = lane + 64 < p.tokens ? row_of<Id>(p.ids, lane + 64, p.vocab) : -1;
+  int64_t task = int64_t{blockIdx.x} * 4 + wave_id();
+  if (task >= p.tasks) {
+    task -= p.tasks;
+    const int64_t row = task / p.column_blocks;
+    if (p.accumulate || row >= p.vocab || __ballot(a == row || b == row) != 0) return;
+    clear<D>(p.dtable, row, task % p.column_blocks, p.d, p.lddtable);
+    return;
+  }
+  const int token = static_cast<int>(task / p.column_blocks);
+  const int64_t c = task % p.column_blocks * 512 + lane * 8, left = p.d - c;
+  const int id = token < 64 ? __builtin_amdgcn_readlane(a, token) : __builtin_amdgcn_readlane(b, token - 64);
+  if (id < 0) return;
+  uint64_t low = __ballot(a == id), high = __ballot(b == id);
+  if ((low ? __builtin_ctzll(low) : 64 + __builtin_ctzll(high)) != token) return;
+  const Value* dy = static_cast<const Value*>(p.dy) + c;
+  constexpr int kAhead = 8;
+  float sum[8] = {};
+  while (low | high) {
+    Eight<X> v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      v[u].zero();
+      int64_t row = -1;
+      if (low) {
+        row = __builtin_ctzll(low);
+        low &= low - 1;
+      } else if (high) {
+        row = 64 + __builtin_ctzll(high);
+        high &= high - 1;
+      }
+      if (row >= 0 && left > 0) v[u].load(dy + row * p.lddy, left);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += v[u][i];
+  }
+  if (left > 0) finish<D>(p, id, c, left, sum);
 }
 
 // A wave adds the rows of one chunk of sorted tokens, 512 columns of them, and gives
@@ -365,11 +417,18 @@ hipError_t launch_lookup(Lookup& p, int id_type, hipStream_t stream) {
 
 template <class X, class D>
 hipError_t launch_sums(Sort& s, Sum& p, int64_t chunks, int id_type, hipStream_t stream) {
+  const int64_t rows = p.accumulate ? 0 : p.vocab * p.column_blocks;    // to be cleared, in pieces of a wave
+  if (p.tokens <= kFewTokens) {
+    p.tasks = p.tokens * p.column_blocks;
+    const unsigned few = static_cast<unsigned>(pieces_of(p.tasks + rows, 4));
+    return id_type == OPT8_ID_INT32 ? queue(few_kernel<X, D, int32_t>, few, 256, stream, p)
+                                    : queue(few_kernel<X, D, int64_t>, few, 256, stream, p);
+  }
   const unsigned groups = static_cast<unsigned>(s.shape.groups);
   hipError_t e = id_type == OPT8_ID_INT32 ? queue(sort_kernel<int32_t>, groups, 64 * kSortWaves, stream, s)
                                           : queue(sort_kernel<int64_t>, groups, 64 * kSortWaves, stream, s);
-  const int64_t sums = p.sum_groups + (p.accumulate ? 0 : pieces_of(p.vocab * p.column_blocks, 4));
-  if (e == hipSuccess && sums > 0) e = queue(sum_kernel<X, D>, static_cast<unsigned>(sums), 256, stream, p);
+  const int64_t sums = p.sum_groups + pieces_of(rows, 4);
+  if (e == hipSuccess) e = queue(sum_kernel<X, D>, static_cast<unsigned>(sums), 256, stream, p);
   if (e == hipSuccess && chunks > 1)
     e = queue(join_kernel<D>, static_cast<unsigned>((chunks - 1) * pieces_of(p.d, 1024)), 256 * kCuts, stream, p);
   return e;
@@ -411,6 +470,8 @@ hipError_t launch_embedding_backward(const opt8_embedding_grad& a, hipStream_t s
   s.keys = reinterpret_cast<int*>(work + space.keys);
   s.starts = reinterpret_cast<int*>(work + space.starts);
   Sum p;
+  p.ids = a.ids;
+  p.tokens = a.tokens;
   p.order = s.order;
   p.keys = s.keys;
   p.starts = s.starts;

@@ -19,6 +19,12 @@ inline int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 inline bool streams(int64_t bytes) { return bytes > int64_t{128} << 20; }
 
 // ---------------------------------------------------------------- embedding's gradient
+// Tokens whose like a wave finds by itself (two in each lane), with no sort.  Whole calls
+// in us, so and with the sort (bf16):  1 x 4096 added: 6.1 8.3   15 x 97 added: 6.0 13.5
+//   128 x 4096 added: 6.5 13.9   102 x 932 into 26413 rows: 12.6 19.4   128 x 4096 into
+//   50257 rows: 57.5 63.8;   of one id only, added: 64 x 4096: 10.1 12.5   128 x 4096: 19.3 13.2
+constexpr int kFewTokens = 128;
+
 // The sort's workgroups, a power of two: each owns one of every `groups` ids in a row
 // (so that ids next to each other, which are often the frequent ones, are not one
 // workgroup's), at most kSortRange of them, counted in LDS.

@@ -115,6 +115,15 @@ def test_gradient(tokens, vocab, d, kind, dtype, out):
     gradient(tokens, vocab, d, dtype, out, I32, True, kind=kind, extra=5, head=3, seed=1)
 
 
+@pytest.mark.parametrize("tokens", [2, 63, 64, 65, 127, 128, 129, 130])
+@pytest.mark.parametrize("kind", ["one", "frequent", "outside"])
+def test_gradient_of_few_tokens(tokens, kind):
+    """Around the number that a wave holds, where the sort begins."""
+    for accumulate in (False, True):
+        gradient(tokens, 11, 530, BF, F32, accumulate=accumulate, kind=kind)
+        gradient(tokens, 70, 20, HF, id_type=I32, accumulate=accumulate, kind=kind, extra=1, seed=1)
+
+
 @pytest.mark.parametrize("tokens,vocab,d,kind", [
     (8191, 50257, 64, "frequent"), (20000, 1000, 40, "frequent"),   # chunks of 8 tokens, and ids over several of them
     (32768, 300, 1024, "even"), (70000, 90, 513, "frequent"),       # chunks of 16 and of 32
