@@ -6,6 +6,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB = os.path.join(HERE, "libopt8.so")
@@ -52,15 +54,26 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: the ROCm toolchain is required to build libopt8.so")
 
 
-def _compile(target: str, sources, verbose: bool) -> str:
-    tmp = target + ".tmp"
-    cmd = [hipcc(), *FLAGS, "-o", tmp, *sources]
+def _run(cmd) -> str:
+    """The compiler's output but for its remark that the host has no packed fp32 instructions."""
     res = subprocess.run(cmd, capture_output=True, text=True)
     out = "\n".join(ln for ln in (res.stdout + res.stderr).splitlines() if "packed-fp32-ops" not in ln)
     if res.returncode != 0:
         raise RuntimeError("hipcc failed:\n" + " ".join(cmd) + "\n" + out)
-    if verbose and out.strip():
-        print(out, file=sys.stderr)
+    return out
+
+
+def _compile(target: str, sources, verbose: bool) -> str:
+    """The sources, each by itself and up to 8 at once, linked into one library."""
+    tmp = target + ".tmp"
+    flags = [f for f in FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as work, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objects = [os.path.join(work, f"{i}.o") for i in range(len(sources))]
+        out = list(pool.map(lambda p: _run([hipcc(), *flags, "-c", "-o", p[0], p[1]]), zip(objects, sources)))
+        out.append(_run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objects]))
+    text = "\n".join(o for o in out if o.strip())
+    if verbose and text:
+        print(text, file=sys.stderr)
     os.replace(tmp, target)
     return target
 
