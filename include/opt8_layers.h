@@ -128,7 +128,7 @@ typedef struct opt8_rms_norm_grad {
   const void* x;             /* [rows, d]                                            */
   const void* weight;        /* [d]; read for dx                                     */
   const float* rstd;         /* [rows]                                               */
-  const void* dsum;          /* [rows, d], or NULL                                   */
+  const void* dsum;          /* [rows, d], or NULL; read for dx                      */
   void* dx;                  /* [rows, d]                                            */
   void* dweight;             /* [d]                                                  */
   void* workspace;           /* 16-byte aligned; read for dweight                    */

@@ -168,7 +168,9 @@ int rms_norm_backward(const opt8_rms_norm_grad* a, void* hip_stream) {
       workspace_of(need > 0 ? a->workspace : nullptr, need),
   };
   if ((rc = check_layers(list, 8))) return rc;
-  return launched(launch_rms_norm_backward(*a, static_cast<hipStream_t>(hip_stream)), "opt8_rms_norm_backward");
+  opt8_rms_norm_grad call = *a;
+  call.dsum = dsum;    // without dx it was not checked, and nothing comes of it
+  return launched(launch_rms_norm_backward(call, static_cast<hipStream_t>(hip_stream)), "opt8_rms_norm_backward");
 }
 
 // ---------------------------------------------------------------- lists of gradients

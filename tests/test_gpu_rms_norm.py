@@ -230,3 +230,17 @@ def test_offsets_past_32_bits():
     ops.opt8_rms_norm_backward(ops.make_rms_norm_grad(y, x, w, rstd, dx, dw, work))
     # h and y are ones but for rounding: each of the columns sums to the rows
     assert bool(((dw - rows).abs() <= rows * 2.0 ** -7).all()) and bool((dx.abs() <= 2.0 ** -6).all())
+
+
+@pytest.mark.parametrize("rows,d", [(300, 64), (37, 4096), (9, 16384), (20, 17000)])
+def test_dweight_alone_has_no_use_for_dsum(rows, d):
+    """The same bits with a dsum of NaN as without one, and as beside dx."""
+    g = torch.Generator().manual_seed(4)
+    x, dy, w, ds = values(rows, d, BF, g), values(rows, d, BF, g), torch.ones(d, dtype=BF, device="cuda"), torch.full((rows, d), float("nan"), dtype=BF, device="cuda")
+    rstd, work = (x.float().square().mean(1) + EPS).rsqrt(), torch.empty(ops.opt8_rms_norm_workspace(rows, d), dtype=torch.uint8, device="cuda")
+    got = []
+    for dx, dsum in [(None, None), (None, ds), (torch.empty_like(x), ds)]:
+        dw = torch.full((d,), 7.0, device="cuda")
+        ops.opt8_rms_norm_backward(ops.make_rms_norm_grad(dy, x, w, rstd, dx, dw, work, dsum=dsum))
+        got.append(dw)
+    assert bool(got[0].isfinite().all()) and torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
