@@ -171,7 +171,8 @@ int opt8_grad_table(const opt8_grad* grads, int32_t n, void* host_table, int64_t
 
 typedef struct opt8_grads {
   const void* table;         /* device copy of a list's table, 8-byte aligned         */
-  int64_t table_bytes;       /* what opt8_grad_table_bytes gave for the list         */
+  int64_t table_bytes;       /* of that copy: what opt8_grad_table_bytes gave, or more
+                                (what lies behind the list's pieces is not read)     */
   double* squares;           /* [1]                                                  */
   float* norm;               /* [1], or NULL                                         */
   void* workspace;           /* 16-byte aligned                                      */

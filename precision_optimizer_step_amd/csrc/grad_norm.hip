@@ -12,9 +12,16 @@ using namespace tile;
 constexpr int kThreads = 256;
 constexpr int kPasses = OPT8_GRAD_PIECE / (kThreads * 8);    // 8 values to a thread in each
 
+// The head's pieces, and no more than the table has room for: a table may be larger than
+// its list's, and what lies behind the list's pieces is not one.
+__device__ __forceinline__ int64_t pieces_there(const GradPiece* pieces, int64_t room) {
+  const int64_t listed = reinterpret_cast<const GradHead*>(pieces - 1)->pieces;
+  return listed < room ? listed : room;
+}
+
 struct NormOf {
   const GradPiece* pieces;    // behind the table's head
-  int64_t count;
+  int64_t room;
   double* sums;       // [groups]
   double* squares;
   float* norm;
@@ -65,9 +72,10 @@ __device__ __forceinline__ void add_squares(const GradPiece& p, bool stream, dou
 __global__ __launch_bounds__(kThreads) void squares_kernel(const NormOf p) {
   double sum[2] = {0.0, 0.0};
   GradPiece next = p.pieces[blockIdx.x];
-  for (int64_t i = blockIdx.x; i < p.count; i += p.groups) {
+  const int64_t count = pieces_there(p.pieces, p.room);
+  for (int64_t i = blockIdx.x; i < count; i += p.groups) {
     const GradPiece piece = next;
-    if (i + p.groups < p.count) next = p.pieces[i + p.groups];
+    if (i + p.groups < count) next = p.pieces[i + p.groups];
     if (piece.type == OPT8_TYPE_BF16) add_squares<Bf16>(piece, p.stream, sum);
     else if (piece.type == OPT8_TYPE_FP16) add_squares<Fp16>(piece, p.stream, sum);
     else add_squares<float>(piece, p.stream, sum);
@@ -92,7 +100,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const NormOf p) {
 
 struct Clip {
   const GradPiece* pieces;    // behind the table's head
-  int64_t count;
+  int64_t room;
   const double* squares;
   float* norm;
   double max_norm;
@@ -135,7 +143,8 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(const Clip p) {
   const double ratio = p.max_norm / (norm + 1e-6);
   const float factor = ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);    // NaN stays NaN
   // pieces with a place of their own come first: all that there is to do by a factor of 1
-  const int64_t count = factor == 1.0f ? reinterpret_cast<const GradHead*>(p.pieces - 1)->own : p.count;
+  const int64_t own = reinterpret_cast<const GradHead*>(p.pieces - 1)->own, all = pieces_there(p.pieces, p.room);
+  const int64_t count = factor == 1.0f && own < all ? own : all;
   for (int64_t i = blockIdx.x; i < count; i += p.groups) {
     const GradPiece piece = p.pieces[i];
     if (piece.type == OPT8_TYPE_BF16) scaled_to<Bf16>(piece, factor);
@@ -152,12 +161,12 @@ int groups_of(int64_t pieces) { return static_cast<int>(std::min<int64_t>(pieces
 hipError_t launch_grad_norm(const opt8_grads& a, hipStream_t stream) {
   NormOf p;
   p.pieces = static_cast<const GradPiece*>(a.table) + 1;
-  p.count = a.table_bytes / OPT8_GRAD_PIECE_BYTES - 1;
+  p.room = a.table_bytes / OPT8_GRAD_PIECE_BYTES - 1;
   p.sums = static_cast<double*>(a.workspace);
   p.squares = a.squares;
   p.norm = a.norm;
-  p.groups = groups_of(p.count);
-  p.stream = streams(p.count * OPT8_GRAD_PIECE * 2);
+  p.groups = groups_of(p.room);
+  p.stream = streams(p.room * OPT8_GRAD_PIECE * 2);
   if (p.groups > 0) {
     const hipError_t e = queue(squares_kernel, static_cast<unsigned>(p.groups), kThreads, stream, p);
     if (e != hipSuccess) return e;
@@ -168,11 +177,11 @@ hipError_t launch_grad_norm(const opt8_grads& a, hipStream_t stream) {
 hipError_t launch_grad_clip(const opt8_grads& a, hipStream_t stream) {
   Clip p;
   p.pieces = static_cast<const GradPiece*>(a.table) + 1;
-  p.count = a.table_bytes / OPT8_GRAD_PIECE_BYTES - 1;
+  p.room = a.table_bytes / OPT8_GRAD_PIECE_BYTES - 1;
   p.squares = a.squares;
   p.norm = a.norm;
   p.max_norm = a.max_norm;
-  p.groups = std::max(1, groups_of(p.count));
+  p.groups = std::max(1, groups_of(p.room));
   return queue(clip_kernel, static_cast<unsigned>(p.groups), kThreads, stream, p);
 }
 

@@ -1,6 +1,8 @@
 """Norm and clipping of a list of gradients against 64-bit forms."""
 
+import ctypes
 import math
+import struct
 
 import pytest
 import torch
@@ -167,3 +169,42 @@ def test_overlaps_are_refused():
             ops.opt8_grad_table(grads, outs)
     ops.opt8_grad_table([t[:50], t[50:]])
     ops.opt8_grad_table([t], [t])
+
+
+@pytest.mark.parametrize("most", [0.5, 1e9])
+def test_a_table_that_held_a_longer_list(most):
+    """A table's memory is used again for a shorter list: what the longer one left behind its pieces does not count."""
+    long = [torch.full((n,), 2.0, dtype=BF, device="cuda") for n in (8192 * 3, 100, 8193)]
+    outs = [torch.full((g.numel(),), 7.0, device="cuda") for g in long]
+    short, place = torch.ones(300, device="cuda"), torch.zeros(300, device="cuda")
+    fns = ops._functions()
+
+    def listed(grads, places):
+        entries = [v for g, o in zip(grads, places) for v in (g.data_ptr(), o.data_ptr(), g.numel(), ops._TYPE[g.dtype], ops._TYPE[o.dtype])]
+        return struct.pack("=" + "QQqii" * len(grads), *entries)
+    size = fns["opt8_grad_table_bytes"](listed(long, outs), 3)
+    assert size == 24 * 7
+    memory = bytearray(size)
+    at = (ctypes.c_char * size).from_buffer(memory)
+    assert fns["opt8_grad_table"](listed(long, outs), 3, at, size) == opt8.OPT8_OK
+    assert fns["opt8_grad_table"](listed([short], [place]), 1, at, size) == opt8.OPT8_OK
+    squares, norm, work = scratch()
+    call = ops.make_grads(torch.frombuffer(memory, dtype=torch.uint8).cuda(), squares, norm, work, max_norm=most)
+    ops.opt8_grad_norm(call)
+    assert float(squares) == 300.0
+    ops.opt8_grad_clip(call)
+    factor = min(1.0, most / (math.sqrt(300.0) + 1e-6))
+    assert torch.equal(place, torch.full_like(place, factor)) and bool((short == 1).all())
+    assert all(bool((g == 2).all()) for g in long) and all(bool((o == 7).all()) for o in outs)
+
+
+def test_nothing_past_a_table_s_bytes_is_read():
+    """A call that names a part of its table takes the pieces in that part, by a factor of 1 too."""
+    g, o = torch.ones(8192 * 4, device="cuda"), torch.zeros(8192 * 4, device="cuda")
+    table = ops.opt8_grad_table([g], [o])
+    squares, norm, work = scratch()
+    call = ops.make_grads(table[:24 * 3], squares, norm, work, max_norm=1e9)
+    ops.opt8_grad_norm(call)
+    assert float(squares) == 2 * 8192
+    ops.opt8_grad_clip(call)
+    assert bool((o[:2 * 8192] == 1).all()) and bool((o[2 * 8192:] == 0).all())
