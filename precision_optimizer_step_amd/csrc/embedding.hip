@@ -360,13 +360,16 @@ __global__ __launch_bounds__(256) void sum_kernel(const Sum p) {
 
 // Adds the partial sums of the id that starts in a chunk and goes on behind it, in the
 // order of the chunks, cut into kCuts stretches: a workgroup takes 1024 columns, 4 to a
-// lane, its waves 256 columns of a stretch each.  Mostly the time to find that there is
-// little to do (6 us of the case above); with one, two and four stretches 65536 tokens of
-// 1024 columns took 99.1, 97.6 and 100.6 us in all, 16384 of one id 88.7, 84.3 and 84.6.
+// lane, its waves 256 columns of a stretch each.  In 64 bits: 2^22 tokens of one id are
+// 2^17 partial sums, and as many additions of like signs in 32 bits drift by thousands
+// of roundings.  Mostly the time to find that there is little to do (6 us of the case
+// above); with one, two and four stretches 65536 tokens of 1024 columns took 99.1, 97.6
+// and 100.6 us in all, 16384 of one id 88.7, 84.3 and 84.6.
 constexpr int kCuts = 2;
+typedef __attribute__((ext_vector_type(4))) double f64x4;
 template <class D>
 __global__ __launch_bounds__(256 * kCuts) void join_kernel(const Sum p) {
-  __shared__ f32x4 parts[kCuts][256];
+  __shared__ f64x4 parts[kCuts][256];
   const int64_t blocks = (p.d + 1023) / 1024;
   const int chunk = static_cast<int>(blockIdx.x / blocks);
   const int total = p.starts[p.shape.groups * p.shape.range];
@@ -382,11 +385,12 @@ __global__ __launch_bounds__(256 * kCuts) void join_kernel(const Sum p) {
   const int each = (chunks + kCuts - 1) / kCuts;
   const int from = cut * each, to = min(from + each, chunks);
   const int count = static_cast<int>(p.d - c < 4 ? p.d - c : 4);
-  f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  f64x4 sum = {0.0, 0.0, 0.0, 0.0};
   const float* at = p.partial + 2 * int64_t{chunk} * p.d + c;
   if (count == 4) {
 #pragma unroll 16
-    for (int k = from; k < to; ++k) sum += *reinterpret_cast<const f32x4_at4*>(at + (k == 0 ? 1 : 2 * int64_t{k}) * p.d);
+    for (int k = from; k < to; ++k)
+      sum += __builtin_convertvector(static_cast<f32x4>(*reinterpret_cast<const f32x4_at4*>(at + (k == 0 ? 1 : 2 * int64_t{k}) * p.d)), f64x4);
   } else {
     for (int k = from; k < to; ++k)
       for (int i = 0; i < 3; ++i)
@@ -401,9 +405,10 @@ __global__ __launch_bounds__(256 * kCuts) void join_kernel(const Sum p) {
   float out[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    out[i] = parts[0][2 * t + i / 4][i % 4];
+    double all = parts[0][2 * t + i / 4][i % 4];
 #pragma unroll
-    for (int s = 1; s < kCuts; ++s) out[i] += parts[s][2 * t + i / 4][i % 4];
+    for (int s = 1; s < kCuts; ++s) all += parts[s][2 * t + i / 4][i % 4];
+    out[i] = static_cast<float>(all);
   }
   finish<D>(p, id, c8, p.d - c8, out);
 }
