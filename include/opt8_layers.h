@@ -95,8 +95,11 @@ int64_t opt8_embedding_workspace(int64_t tokens, int64_t vocab, int64_t d);
  *   q, scale   codes of n and their scales, as opt8_fp8_quantize gives them by rows
  *         (OPT8_FP8_BLOCK_ROW; scale [ceil(d/128), rows]): operand a of opt8_fp8_matmul
  *   rstd  fp32 [rows], for the backward pass
- * The mean is an fp32 sum of squares, which has to stay below 2^128 (beyond it rstd is 0).  sum may
- * be the same matrix as residual or x (the same address and ld). */
+ * The squares are added up in 64 bits and rstd is rounded once, so a row of finite t
+ * has its formula's values also where its squares leave fp32.  With eps == 0 a row of
+ * zeros has an infinite rstd, and so has one whose rstd fp32 cannot hold (a root below
+ * 2^-128); a root above 2^126 has a subnormal rstd, of fewer bits.  sum may be the same
+ * matrix as residual or x (the same address and ld). */
 typedef struct opt8_rms_norm {
   const void* x;             /* [rows, d]                                            */
   const void* residual;      /* [rows, d], or NULL                                   */

@@ -244,3 +244,35 @@ def test_dweight_alone_has_no_use_for_dsum(rows, d):
         ops.opt8_rms_norm_backward(ops.make_rms_norm_grad(dy, x, w, rstd, dx, dw, work, dsum=dsum))
         got.append(dw)
     assert bool(got[0].isfinite().all()) and torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+@pytest.mark.parametrize("d", [1, 7, 128, 500, 1000, 2048, 4096, 8192, 16384, 20000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_whose_squares_leave_fp32(d, dtype):
+    """Without eps the norm does not change with its row's size: rows of 2^-125 to 2^125, whose squares are
+    0 or infinite in 32 bits, have the formula's values; smaller ones have an infinite rstd, as zeros have."""
+    g = torch.Generator().manual_seed(6)
+    sizes = torch.tensor([-125.0, -100, -80, -75, -64, -63, -40, 0, 40, 63, 64, 80, 100, 121])
+    x = torch.rand(len(sizes), d, generator=g) * 0.5 + 0.75
+    x = (x * torch.where(torch.rand(x.shape, generator=g) < 0.5, -1.0, 1.0) * 2.0 ** sizes[:, None]).to(dtype).cuda()
+    w = torch.ones(d, dtype=dtype, device="cuda")
+    for residual in (None, x * 0.5):
+        y, s, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(len(sizes), device="cuda")
+        ops.opt8_rms_norm_forward(ops.make_rms_norm(x, w, y=y, rstd=rstd, residual=residual, sum=None if residual is None else s, eps=0.0))
+        want = lref.norm(x.cpu(), w.cpu(), 0.0, None if residual is None else residual.cpu())
+        lref.check("rstd", rstd, *want["rstd"])
+        lref.check("y", y, *want["n"])
+    small = torch.full((2, d), 2.0 ** -131, dtype=dtype, device="cuda")
+    small[1] = 0
+    ops.opt8_rms_norm_forward(ops.make_rms_norm(small, w, rstd=rstd[:2], eps=0.0))
+    assert rstd[:2].tolist() == [float("inf")] * 2
+
+
+@pytest.mark.parametrize("rows,d", [(300, 128), (37, 4096), (5, 20000)])
+def test_rstd_is_rounded_once(rows, d):
+    """Half a step of fp32 and what 64-bit sums leave of it."""
+    x = values(rows, d, BF, torch.Generator().manual_seed(7), scale=3.0)
+    rstd = torch.empty(rows, device="cuda")
+    ops.opt8_rms_norm_forward(ops.make_rms_norm(x, torch.ones(d, dtype=BF, device="cuda"), rstd=rstd, eps=EPS))
+    want = (x.double().square().mean(1) + EPS) ** -0.5
+    assert bool(((rstd.double() - want).abs() <= lref.U * (1 + 2.0 ** -20) * want).all())
