@@ -18,6 +18,15 @@ inline int64_t align16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 // 64032 x 128 norms 6.9 and 7.6 us, 4001 x 1600 backward 15.0 and 17.4.
 inline bool streams(int64_t bytes) { return bytes > int64_t{128} << 20; }
 
+// Whether the norm's 16-bit y is stored through the caches, for a product that reads it
+// again for each of its tiles.  Norm and gated block in a row, y through the caches and
+// past them, us:  4096 wide, f 4096:  64 rows: 24.0 28.5   333: 39.1 52.0   1000: 64.6 70.4
+//   1500: 89.5 93.2   1750: 97.0 98.2   2048: 105.8 105.4   4096: 211 213;  1024 wide:
+//   333: 16.7 19.3   1500: 32.1 33.8   4000: 68.5 69.5   6000: 100.3 99.9.  The norm alone:
+//   333 x 4096: 4.2 3.8   2048: 12.8 11.3   16384: 98.8 91.6.  (A reader that takes
+// a result once does not mind: lookup and norm 6.8 and 6.9 at 333 rows, 10.6 and 9.6 at 1000.)
+inline bool stays(int64_t bytes) { return bytes <= int64_t{8} << 20; }
+
 // ---------------------------------------------------------------- embedding's gradient
 // Tokens whose like a wave finds by itself (two in each lane), with no sort.  Whole calls
 // in us, so and with the sort (bf16):  1 x 4096 added: 6.1 8.3   15 x 97 added: 6.0 13.5

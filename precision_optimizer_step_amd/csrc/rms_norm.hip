@@ -77,7 +77,7 @@ struct Norm {
   float* rstd;
   int64_t rows, d, ldx, ldresidual, ldsum, ldy, ldq;
   double eps, mean;   // mean: 1 / d
-  int wide_weight, stream;
+  int wide_weight, stream, stays;
 };
 
 // Squares are added up in 64 bits: no row of finite values is too large or too small for
@@ -111,7 +111,11 @@ __device__ __forceinline__ void norm_out(const Norm& p, int64_t row, int64_t c, 
   float n[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) n[i] = (t[i] * rstd) * w[i];
-  if (p.y && left > 0) stream_eight<X>(static_cast<typename Raw<X>::type*>(p.y) + row * p.ldy + c, n, left);
+  if (p.y && left > 0) {
+    auto* to = static_cast<typename Raw<X>::type*>(p.y) + row * p.ldy + c;
+    if (p.stays) store_eight<X>(to, n, left);
+    else stream_eight<X>(to, n, left);
+  }
   if constexpr (F >= 0) {
     float top = 0.0f;
 #pragma unroll
@@ -520,6 +524,7 @@ hipError_t launch_rms_norm_forward(const opt8_rms_norm& a, hipStream_t stream) {
   p.mean = 1.0 / static_cast<double>(a.d);
   p.wide_weight = a.weight_type == OPT8_TYPE_FP32 && a.type != OPT8_TYPE_FP32;
   p.stream = streams(a.rows * a.d * (a.residual ? 6 : 4));
+  p.stays = stays(a.rows * a.d * 2);
   if (a.type == OPT8_TYPE_BF16) return launch_codes<Bf16>(p, a.q_type, stream);
   if (a.type == OPT8_TYPE_FP16) return launch_codes<Fp16>(p, a.q_type, stream);
   return launch_codes<float>(p, a.q_type, stream);
