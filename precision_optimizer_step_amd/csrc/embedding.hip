@@ -83,9 +83,9 @@ __device__ __forceinline__ int slot_of(int id, const SortShape& s) { return owne
 // they stand, and then gives them their positions.  Waves read consecutive stretches,
 // and each has its own counter for every id, so that a token's position depends on the
 // ids alone.  A wave that finds more than it can note (where one id has over 512 of its
-// stretch's tokens) reads its stretch again.  256 workgroups read 16384 ids in 9.4 us,
-// 1001 in 5.8; with an adjacent range of ids to each, where a few workgroups have the
-// frequent ones, 94 and 10.5.
+// stretch's tokens) reads its stretch again.  256 workgroups read 16384 ids in 9.4
+// to 11.5 us, 1001 in 6.0, 65536 in 28.7; with an adjacent range of ids to each, where a
+// few workgroups have the frequent ones, 16384 took 94 and 1001 10.5.
 struct Sort {
   const void* ids;
   int64_t tokens, vocab;
@@ -362,9 +362,10 @@ __global__ __launch_bounds__(256) void sum_kernel(const Sum p) {
 // order of the chunks, cut into kCuts stretches: a workgroup takes 1024 columns, 4 to a
 // lane, its waves 256 columns of a stretch each.  In 64 bits: 2^22 tokens of one id are
 // 2^17 partial sums, and as many additions of like signs in 32 bits drift by thousands
-// of roundings.  Mostly the time to find that there is little to do (6 us of the case
-// above); with one, two and four stretches 65536 tokens of 1024 columns took 99.1, 97.6
-// and 100.6 us in all, 16384 of one id 88.7, 84.3 and 84.6.
+// of roundings.  Mostly the time to find that there is little to do (7 us of the case
+// above); with one, two and four stretches 65536 tokens of 1024 columns take 82.4, 81.0
+// and 83.1 us in all, 16384 of 4096 columns and one id 80.5, 75.5 and 75.3, 1001 of 1600 17.5,
+// 16.5 and 16.4.
 constexpr int kCuts = 2;
 typedef __attribute__((ext_vector_type(4))) double f64x4;
 template <class D>

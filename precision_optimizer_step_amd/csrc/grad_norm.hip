@@ -135,7 +135,7 @@ __device__ __forceinline__ void scaled_to(const GradPiece& p, float factor) {
   else scaled<X, float>(p, factor);
 }
 
-// 355M fp32 values to bf16: 353 us for 2.1 GB (6.0 TB/s).  With a factor of 1 the list's
+// 355M fp32 values to bf16: 370 us for 2.1 GB (5.8 TB/s).  With a factor of 1 the list's
 // pieces in place are not even looked up (324,000 of them: 4 us; looked up one by one 68).
 __global__ __launch_bounds__(kThreads) void clip_kernel(const Clip p) {
   const double norm = __builtin_sqrt(*p.squares);

@@ -90,9 +90,10 @@ inline RowShape norm_grad_shape(int64_t d) {
   if (d <= 8192) return {1024, 1};
   return {1024, 2};
 }
-// Workgroups that each keep a sum of dweight, and so rows of the workspace: two to a CU
-// (16384 x 4096 bf16 with dsum, both kernels: 101 us; 384 of them 100, 768 105, 1024 114,
-// 256 128; 4001 x 1600 fp16: 15.2, 16.5, 14.6, 15.3 and 20.8).
+// Workgroups that each keep a sum of dweight, and so rows of the workspace: two to a CU.
+// Both kernels in us with 256, 384, 512, 768 and 1024 of them:  16384 x 4096 bf16 with dsum:
+// 126 98.7 95.7 99.1 110   16384 x 2048: 89 65 55.4 52.3 54.9   4001 x 1600 fp16: 21.4 17.1
+//   15.5 14.8 15.5   64032 x 128: 20.0 16.6 15.3 15.1 15.7   500 x 4096: 10.5 11.1 12.1 12.1 12.1
 inline int64_t norm_grad_groups(int64_t rows, int64_t d) {
   if (d > kNormHeld) return std::max<int64_t>(1, std::min<int64_t>(64, rows / 8));
   const int64_t lanes = norm_grad_shape(d).lanes;
@@ -105,9 +106,9 @@ inline int64_t norm_grad_space(int64_t rows, int64_t d) {
 }
 
 // ---------------------------------------------------------------- gradients' norm
-// Workgroups, 4 to a CU (355M fp32 values, norm and clipping to bf16: 598 us; 512 of
-// them 765, 768 622, 1536 666, 2048 635; 2.65G bf16 values, norm only: 882, 1091, 867,
-// 1014 and 892).
+// Workgroups, 4 to a CU.  With 512, 768, 1024, 1536 and 2048 of them, in us:  355M fp32
+// values, norm and clipping to bf16: 701 625 608 624 635;  2.65G bf16 values, norm only: 1038 801
+// 784 776 804.
 constexpr int64_t kGradGroups = 1024;
 
 }  // namespace opt8

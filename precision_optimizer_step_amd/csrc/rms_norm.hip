@@ -193,7 +193,9 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_kernel(const N
   }
 }
 
-// Longer rows are read twice, by a workgroup each.
+// Longer rows are read twice, by a workgroup each: 3000 x 20000 bf16 with residual, y and
+// codes 120 us, 782 MB with the second reading (6.5 TB/s, part of it from the caches); fp32
+// without residual 112.
 template <class X, int F>
 __global__ __launch_bounds__(1024) void norm_long_kernel(const Norm p) {
   __shared__ double slots[16];
@@ -283,8 +285,10 @@ __device__ __forceinline__ void give_dweight(const NormGrad& p, int64_t c, const
 // As norm_kernel, but a workgroup walks through the rows, every p.groups-th of them
 // (or of their groups), and keeps its sums of dweight in registers; the next row is
 // on its way while one is computed.  Bound by memory: 16384 x 4096 bf16 with dsum 89-93
-// us, 546 MB (6 TB/s).  The widest form (over 8192 columns) spills registers, 92 bytes of a
-// lane with 16-bit rows: 4096 x 16384 121 us for the same bytes.
+// us, 546 MB (6 TB/s).  The widest form (over 8192 columns) spills registers, 84 bytes of a
+// lane with 16-bit rows: 4096 x 16384 122 us for the same bytes.  Few or short rows are
+// bound by the bytes under way, a row (or 16 short ones) to a workgroup at a time, 13 to 16
+// KB to a CU: 4001 x 1600 fp16 38 MB in 12.8 us, 64032 x 128 49 MB in 12 (3 and 4 TB/s).
 template <class X, int LANES, int K>
 __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_grad_kernel(const NormGrad p) {
   constexpr int kThreads = LANES > 256 ? LANES : 256, kRows = kThreads / LANES;
@@ -383,7 +387,8 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_grad_kernel(co
 }
 
 // Rows too long to be held: sums of dweight by columns, a thread 8 of them over every
-// p.groups-th row.
+// p.groups-th row.  With dx below, dy and x are read three times: 3000 x 20000 bf16 with dsum
+// 155 us, 50 of them here.
 template <class X>
 __global__ __launch_bounds__(256) void dweight_long_kernel(const NormGrad p) {
   typedef typename Raw<X>::type Value;
