@@ -60,8 +60,9 @@ typedef struct opt8_embedding {
 } opt8_embedding;
 int opt8_embedding_forward(const opt8_embedding* embedding, void* hip_stream);
 
-/* dtable[v] = scale * (sum of dy[i] over the tokens i whose id is v), summed in fp32
- * in an order that depends on the ids alone, rounded once.  Tokens whose id is no
+/* dtable[v] = scale * (sum of dy[i] over the tokens i whose id is v), summed in an
+ * order that depends on the ids alone (in fp32 up to 128 tokens, in 64 bits what such
+ * parts of more give), rounded once.  Tokens whose id is no
  * row of the table are left out, whatever their dy.  accumulate == 0: every row of
  * dtable is written, those without a token with zeros (bf16: the gradient that
  * opt8_adamw_step reads).  accumulate != 0: the sum is added to what the row holds,
